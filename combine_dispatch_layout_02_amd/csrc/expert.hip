@@ -1,0 +1,229 @@
+// expert.hip -- the experts' products over fp8 rows, for gfx950: e4m3 rows
+// with one fp32 scale per 128 elements times e4m3 weights with one fp32 scale
+// per 128 x 128 block, grouped by the experts' row segments.
+//
+//   y[s, n] = sum_b as[s, b] ws[e, n / 128, b] sum_{i < 128} a[s, 128 b + i] w[e, n, 128 b + i]
+//
+// The inner sum of one block is one v_mfma_f32_16x16x128_f8f6f4 (products of
+// two e4m3 values are exact in binary32); its 4 values per lane are then
+// multiplied by the two scales and added to the binary32 accumulator.  The
+// weights are the matrix instruction's first operand, the rows its second: a
+// lane's 4 values then share one row (lane % 16) and lie at consecutive n, so
+// the row's scale is one register per lane and the result one wide store.
+#include "ep_device.h"
+#include "moe.h"
+
+namespace ep {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+// D = A B over 128 e4m3 values per row and column.  Lane l holds 32 bytes of
+// row (or column) l % 16; the two operands name their 128 values in the same
+// order, whichever it is.  D: row 4 (l / 16) + i, column l % 16.
+__device__ __forceinline__ f32x4 mfma_128(i32x8 a, i32x8 b) {
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
+// A lane's 32 bytes of a 128-byte block: 16 at 16 (l / 16), 16 more 64 on, so
+// that one load instruction covers whole 64-byte pieces of 16 rows.
+__device__ __forceinline__ i32x8 ld_operand(const uint8_t *p) {
+    const vec16 lo = ld16(p), hi = ld16(p + 64);
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// The rows of expert e in a and the output, clamped into [0, rows].
+__device__ __forceinline__ void expert_rows(const int32_t *off, const ExpertShape &s, int e, int *lo, int *hi) {
+    const int rows = (int)s.rows;
+    int b = off[e], t = off[e + 1];
+    if (s.M > 0) {
+        const int r = e / (s.E / s.R), first = off[r * (s.E / s.R)];
+        const int end = (r + 1) * s.M;
+        b = min(b - first + r * s.M, end);
+        t = min(t - first + r * s.M, end);
+    }
+    b = min(max(b, 0), rows);
+    *lo = b;
+    *hi = min(max(t, b), rows);
+}
+
+// Row tiles of BM rows are numbered without a pass over the experts first:
+// expert e's tiles are off[e] / BM + e and on.  As floor((o + n) / BM) + 1 >=
+// floor(o / BM) + ceil(n / BM), no two experts share a number, and rows / BM +
+// E numbers suffice; those without a tile end at once.  Every thread looks at
+// its share of the experts; the one that finds the tile names the expert.
+__device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape &s, int slot, int BM, int *found,
+                                          int *expert, int *row, int *end) {
+    if (threadIdx.x == 0) *found = -1;
+    __syncthreads();
+    for (int e = threadIdx.x; e < s.E; e += blockDim.x) {
+        int lo, hi;
+        expert_rows(off, s, e, &lo, &hi);
+        const int first = max(off[e], 0) / BM + e;
+        if (slot >= first && slot - first < (hi - lo + BM - 1) / BM) *found = e;
+    }
+    __syncthreads();
+    const int e = *found;
+    if (e < 0) return false;
+    int lo, hi;
+    expert_rows(off, s, e, &lo, &hi);
+    const int r0 = lo + (slot - (max(off[e], 0) / BM + e)) * BM;
+    *expert = e;
+    *row = r0;
+    *end = hi;
+    return r0 >= lo && r0 < hi;   // offsets that do not ascend: no tile
+}
+
+// h = g / (1 + e^-g) u
+__device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+
+constexpr int kColWaves = 8;   // waves side by side: 16 weight rows twice each
+
+// BM = 16 MT rows by 256 weight rows (gated: 128 columns of gate and the same
+// 128 of up, one scale group of the result), K split over KS waves whose
+// parts are added in LDS in wave order.  Operands go straight from memory to
+// registers.
+template <int MT, int KS, bool GATED>
+__global__ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
+    ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
+    uint16_t *out, uint8_t *oq, float *oqs) {
+    __shared__ int found;
+    __shared__ f32x4 part[KS > 1 ? KS - 1 : 1][KS > 1 ? kColWaves : 1][KS > 1 ? 2 * MT : 1][kWave];
+    __shared__ float amax[GATED ? kColWaves : 1][GATED ? 16 * MT : 1];
+    int e, row, end;
+    if (!find_tile(off, s, blockIdx.x, 16 * MT, &found, &e, &row, &end)) return;
+
+    const int lane = threadIdx.x & (kWave - 1), wid = threadIdx.x / kWave;
+    const int col = wid % kColWaves, ks = wid / kColWaves;
+    const int r16 = lane & 15, quad = lane >> 4;
+    const int KB = s.K / 128;
+    const int wrows = GATED ? 2 * s.N : s.N;
+    // the two groups of 16 weight rows of this wave
+    const int n0 = GATED ? (int)blockIdx.y * 128 + col * 16 : (int)blockIdx.y * 256 + col * 32;
+    const int n1 = GATED ? n0 + s.N : n0 + 16;
+    const uint8_t *we = w + (size_t)e * wrows * s.K;
+    const float *wse = ws + (size_t)e * ((wrows + 127) / 128) * KB;
+    const uint8_t *w0 = we + (size_t)min(n0 + r16, wrows - 1) * s.K + quad * 16;
+    const uint8_t *w1 = we + (size_t)min(n1 + r16, wrows - 1) * s.K + quad * 16;
+    const float *ws0 = wse + (size_t)(min(n0, wrows - 1) / 128) * KB;
+    const float *ws1 = wse + (size_t)(min(n1, wrows - 1) / 128) * KB;
+    const uint8_t *ap[MT];
+    const float *asp[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int r = min(row + 16 * m + r16, end - 1);   // rows past the segment repeat its last one
+        ap[m] = a + (size_t)r * s.K + quad * 16;
+        asp[m] = as + (size_t)r * KB;
+    }
+
+    f32x4 acc[2][MT] = {};
+    const int kb0 = KB * ks / KS, kb1 = KB * (ks + 1) / KS;
+    for (int kb = kb0; kb < kb1; ++kb) {
+        const i32x8 f0 = ld_operand(w0 + (size_t)kb * 128), f1 = ld_operand(w1 + (size_t)kb * 128);
+        const float c0 = ws0[kb], c1 = ws1[kb];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const i32x8 x = ld_operand(ap[m] + (size_t)kb * 128);
+            const float sc = asp[m][kb];
+            const f32x4 d0 = mfma_128(f0, x), d1 = mfma_128(f1, x);
+            const float s0 = sc * c0, s1 = sc * c1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[0][m][i] = __builtin_fmaf(d0[i], s0, acc[0][m][i]);
+                acc[1][m][i] = __builtin_fmaf(d1[i], s1, acc[1][m][i]);
+            }
+        }
+    }
+    if constexpr (KS > 1) {
+        if (ks > 0)
+#pragma unroll
+            for (int m = 0; m < 2 * MT; ++m) part[ks - 1][col][m][lane] = acc[m & 1][m >> 1];
+        __syncthreads();
+        if (ks == 0)
+#pragma unroll
+            for (int p = 0; p < KS - 1; ++p)
+#pragma unroll
+                for (int m = 0; m < 2 * MT; ++m) acc[m & 1][m >> 1] += part[p][col][m][lane];
+    }
+
+    if constexpr (!GATED) {
+        if (ks > 0) return;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int r = row + 16 * m + r16;
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                const int n = n0 + 16 * f + 4 * quad;   // N % 8 == 0: all 4 in or all out
+                if (r >= end || n >= s.N) continue;
+                uint2 v;
+                v.x = pack_bf16x2(acc[f][m][0], acc[f][m][1]);
+                v.y = pack_bf16x2(acc[f][m][2], acc[f][m][3]);
+                *reinterpret_cast<uint2 *>(out + (size_t)r * s.N + n) = v;
+            }
+        }
+    } else {
+        f32x4 h[MT];
+        if (ks == 0) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    h[m][i] = gate(acc[0][m][i], acc[1][m][i]);
+                    top = fmaxf(top, fabsf(h[m][i]));
+                }
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                if (quad == 0) amax[col][16 * m + r16] = top;
+            }
+        }
+        __syncthreads();
+        if (ks > 0) return;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const int r = row + 16 * m + r16;
+            float top = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kColWaves; ++c) top = fmaxf(top, amax[c][16 * m + r16]);
+            const float scale = (top == 0.0f) ? 1.0f : top / 448.0f;
+            uint32_t q = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q |= f32_to_e4m3(h[m][i] / scale) << (8 * i);
+            if (r >= end) continue;
+            *reinterpret_cast<uint32_t *>(oq + (size_t)r * s.N + n0 + 4 * quad) = q;
+            if (col == 0 && quad == 0) oqs[(size_t)r * (s.N / 128) + blockIdx.y] = scale;
+        }
+    }
+}
+
+constexpr int kStreamMT = 4, kStreamKS = 1;
+
+int64_t tile_slots(const ExpertShape &s, int BM) { return s.rows / BM + s.E; }
+
+}  // namespace
+
+bool expert_grid_fits(const ExpertShape &s, bool gated) {
+    const int64_t cols = gated ? s.N / 128 : (s.N + 255) / 256;
+    return cols <= 65535 && tile_slots(s, 16) * 1024 < (int64_t(1) << 32);
+}
+
+hipError_t launch_expert_gemm(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
+                              const uint8_t *w, const float *ws, uint16_t *out, hipStream_t stream) {
+    const dim3 grid((unsigned)tile_slots(s, 16 * kStreamMT), (unsigned)((s.N + 255) / 256));
+    hipLaunchKernelGGL((ep_expert_stream_kernel<kStreamMT, kStreamKS, false>), grid,
+                       dim3(kWave * kColWaves * kStreamKS), 0, stream, s, offset, a, as, w, ws, out, nullptr, nullptr);
+    return hipGetLastError();
+}
+
+hipError_t launch_expert_gated(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
+                               const uint8_t *w, const float *ws, uint8_t *q, float *qs, hipStream_t stream) {
+    const dim3 grid((unsigned)tile_slots(s, 16 * kStreamMT), (unsigned)(s.N / 128));
+    hipLaunchKernelGGL((ep_expert_stream_kernel<kStreamMT, kStreamKS, true>), grid,
+                       dim3(kWave * kColWaves * kStreamKS), 0, stream, s, offset, a, as, w, ws, nullptr, q, qs);
+    return hipGetLastError();
+}
+
+}  // namespace ep

@@ -37,6 +37,7 @@ EXPORTED = (
     "ep_dispatch_ranks", "ep_expert_reduce_ranks", "ep_combine_ranks", "ep_quant_fp8_s128",
     "ep_expert_scale_bf16", "ep_expert_requant_mxfp8", "ep_expert_requant_nvfp4", "ep_accounting",
     "ep_calib_copy", "ep_stream", "ep_dispatch_with_layout_static", "ep_plan_info",
+    "ep_route", "ep_route_backward", "ep_expert_gemm", "ep_expert_gated", "ep_combine_backward",
 )
 
 
@@ -65,6 +66,34 @@ class ep_shape(ctypes.Structure):
     def rank_rows_cap(self) -> int:
         """Receive rows of the (token, rank) layout: T * min(k, R)."""
         return self.num_tokens * min(self.num_topk, self.num_ranks)
+
+
+EP_SCORE_SOFTMAX, EP_SCORE_SIGMOID = 0, 1
+
+
+class ep_router(ctypes.Structure):
+    _fields_ = [
+        ("num_experts", ctypes.c_int32),
+        ("num_topk", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_top", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("logits_bf16", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class ep_expert_shape(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("num_experts", ctypes.c_int32),
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("num_ranks", ctypes.c_int32),
+        ("rank_capacity", ctypes.c_int32),
+    ]
 
 
 class ep_accounting_t(ctypes.Structure):
@@ -128,7 +157,7 @@ def load():
                            "python combine_dispatch_layout_02_amd/build.py)")
     lib = ctypes.CDLL(LIB_PATH)
     P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-    SP = ctypes.POINTER(ep_shape)
+    SP, RP, XP = ctypes.POINTER(ep_shape), ctypes.POINTER(ep_router), ctypes.POINTER(ep_expert_shape)
     sig = {
         "ep_abi_version": (ctypes.c_int, []),
         "ep_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -156,6 +185,11 @@ def load():
         "ep_stream": (ctypes.c_int, [i32, P, P, sz, sz, i32, P]),
         "ep_dispatch_with_layout_static": (ctypes.c_int, [SP] + [P] * 15 + [P]),
         "ep_plan_info": (ctypes.c_int, [SP, ctypes.POINTER(ep_plan_info_t)]),
+        "ep_route": (ctypes.c_int, [RP, i64, P, P, P, P, P]),
+        "ep_route_backward": (ctypes.c_int, [RP, i64, P, P, P, P, P]),
+        "ep_expert_gemm": (ctypes.c_int, [XP, P, P, P, P, P, P, P]),
+        "ep_expert_gated": (ctypes.c_int, [XP, P, P, P, P, P, P, P, P]),
+        "ep_combine_backward": (ctypes.c_int, [SP, P, P, P, P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -531,6 +565,123 @@ def ep_expert_requant_nvfp4(shape, expert_offset, factor, recv, out_q, out_scale
         "ep_expert_requant_nvfp4")
 
 
+# --------------------------------------------------------------------------- router, experts, gradients
+
+_SCORES = {"softmax": EP_SCORE_SOFTMAX, "sigmoid": EP_SCORE_SIGMOID}
+
+
+def make_router(E, k, score="softmax", num_groups=1, topk_groups=None, group_top=None, renormalize=False,
+                scale=1.0) -> ep_router:
+    """How ep_route chooses: E experts, the k best, `score` "softmax" or
+    "sigmoid"; groups with the sum of their `group_top` best keys (2 where a
+    group holds two) as their mark, `topk_groups` of them kept (all, if not
+    given); weights over their sum with `renormalize`, times `scale`."""
+    if score not in _SCORES:
+        raise ValueError(f"score: expected one of {sorted(_SCORES)}, got {score!r}")
+    if group_top is None:
+        group_top = 2 if num_groups > 1 and E // num_groups > 1 else 1
+    return ep_router(int(E), int(k), _SCORES[score], int(num_groups),
+                     int(num_groups if topk_groups is None else topk_groups), int(group_top), int(bool(renormalize)),
+                     0, float(scale))
+
+
+def _on_current(*tensors):
+    """Every tensor given lives on the current device (the launch goes there)."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+    for t in tensors:
+        if t is not None and t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
+def _router_for(router, logits):
+    if logits.dtype not in (torch.float32, torch.bfloat16) or logits.dim() != 2 \
+            or logits.shape[1] != router.num_experts:
+        raise ValueError(f"logits: expected float32 or bfloat16 (T, {router.num_experts}), got {logits.dtype} "
+                         f"{tuple(logits.shape)}")
+    r = ep_router.from_buffer_copy(router)
+    r.logits_bf16 = int(logits.dtype == torch.bfloat16)
+    return r
+
+
+def ep_route(router, logits, bias, topk_idx, topk_w, stream=None):
+    """Experts and weights of each row of logits ([T, E] fp32 or bf16)."""
+    r = _router_for(router, logits)
+    T, k = logits.shape[0], r.num_topk
+    if bias is not None:
+        _need(bias, torch.float32, (r.num_experts,), "bias")
+    _need(topk_idx, torch.int64, (T, k), "topk_idx")
+    _need(topk_w, torch.float32, (T, k), "topk_w")
+    _on_current(logits, bias, topk_idx, topk_w)
+    _ok(load().ep_route(ctypes.byref(r), T, _ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(topk_w),
+                        _stream(stream)), "ep_route")
+
+
+def ep_route_backward(router, logits, topk_idx, grad_topk_w, grad_logits, stream=None):
+    """Gradient of ep_route's weights over its logits, the choice held fixed."""
+    r = _router_for(router, logits)
+    T, k = logits.shape[0], r.num_topk
+    _need(topk_idx, torch.int64, (T, k), "topk_idx")
+    _need(grad_topk_w, torch.float32, (T, k), "grad_topk_w")
+    _need(grad_logits, logits.dtype, logits.shape, "grad_logits")
+    _on_current(logits, topk_idx, grad_topk_w, grad_logits)
+    _ok(load().ep_route_backward(ctypes.byref(r), T, _ptr(logits), _ptr(topk_idx), _ptr(grad_topk_w),
+                                 _ptr(grad_logits), _stream(stream)), "ep_route_backward")
+
+
+def _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity) -> ep_expert_shape:
+    if a.dim() != 2 or w.dim() != 3 or a.shape[1] % 128:
+        raise ValueError("expected a (rows, K), w (experts, N, K), K a multiple of 128")
+    rows, K = a.shape
+    E, wide = w.shape[:2]
+    _need(expert_offset, torch.int32, (E + 1,), "expert_offset")
+    _need(a, torch.uint8, (rows, K), "a")
+    _need(a_scales, torch.float32, (rows, K // 128), "a_scales")
+    _need(w, torch.uint8, (E, wide, K), "w")
+    _need(w_scales, torch.float32, (E, (wide + 127) // 128, K // 128), "w_scales")
+    _on_current(expert_offset, a, a_scales, w, w_scales)
+    return ep_expert_shape(rows, E, K, N, int(num_ranks), int(rank_capacity))
+
+
+def ep_expert_gemm(expert_offset, a, a_scales, w, w_scales, out, num_ranks=1, rank_capacity=0, stream=None):
+    """Each expert's FP8_S128 rows times its block-scaled e4m3 weights
+    [E, N, K] into bf16 rows; num_ranks and rank_capacity for RANK_MAJOR rows."""
+    N = w.shape[1]
+    sh = _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity)
+    _need(out, torch.bfloat16, (sh.rows, N), "out")
+    _on_current(out)
+    _ok(load().ep_expert_gemm(ctypes.byref(sh), _ptr(expert_offset), _ptr(a), _ptr(a_scales), _ptr(w),
+                              _ptr(w_scales), _ptr(out), _stream(stream)), "ep_expert_gemm")
+
+
+def ep_expert_gated(expert_offset, a, a_scales, w, w_scales, out_q, out_scales, num_ranks=1, rank_capacity=0,
+                    stream=None):
+    """silu(gate) * up of each expert's FP8_S128 rows with its block-scaled
+    e4m3 weights [E, 2 N, K] (gate rows, then up rows) into FP8_S128 rows."""
+    if w.shape[1] % 256:
+        raise ValueError("w: expected (experts, 2 N, K) with N a multiple of 128")
+    N = w.shape[1] // 2
+    sh = _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity)
+    _need(out_q, torch.uint8, (sh.rows, N), "out_q")
+    _need(out_scales, torch.float32, (sh.rows, N // 128), "out_scales")
+    _on_current(out_q, out_scales)
+    _ok(load().ep_expert_gated(ctypes.byref(sh), _ptr(expert_offset), _ptr(a), _ptr(a_scales), _ptr(w),
+                               _ptr(w_scales), _ptr(out_q), _ptr(out_scales), _stream(stream)), "ep_expert_gated")
+
+
+def ep_combine_backward(shape, dy, expert_out, token_slot, topk_w, grad_expert_out, grad_topk_w, stream=None):
+    """Gradients of ep_combine (bf16 payload) over expert_out and topk_w."""
+    T, k, H = shape.num_tokens, shape.num_topk, shape.hidden
+    _need(dy, torch.bfloat16, (T, H), "dy")
+    _need(expert_out, torch.bfloat16, (shape.rows, H), "expert_out")
+    _need(token_slot, torch.int32, (T, k), "token_slot")
+    _need(topk_w, torch.float32, (T, k), "topk_w")
+    _need(grad_expert_out, torch.bfloat16, (shape.rows, H), "grad_expert_out")
+    _need(grad_topk_w, torch.float32, (T, k), "grad_topk_w")
+    _on_current(dy, expert_out, token_slot, topk_w, grad_expert_out, grad_topk_w)
+    _ok(load().ep_combine_backward(ctypes.byref(shape), _ptr(dy), _ptr(expert_out), _ptr(token_slot), _ptr(topk_w),
+                                   _ptr(grad_expert_out), _ptr(grad_topk_w), _stream(stream)), "ep_combine_backward")
+
+
 def ep_accounting(shape, own_node, num_tokens_per_rank, num_tokens_per_node, rdma_algo_token_count,
                   valid_pairs) -> dict:
     """Host arithmetic on host copies of the counts (numpy int32 arrays)."""
@@ -725,3 +876,45 @@ def combine_ranks(partial, handle: RankHandle, stream=None):
     y = torch.empty((sh.num_tokens, sh.hidden), dtype=torch.bfloat16, device=partial.device)
     ep_combine_ranks(sh, partial, handle.token_rank_slot, y, stream)
     return y
+
+
+# --------------------------------------------------------------------------- router, experts, gradients (allocating)
+
+def route(logits, router, bias=None, stream=None):
+    """Returns topk_idx (int64, -1: no expert left) and topk_w (fp32), both [T, k]: what dispatch takes."""
+    T, k = logits.shape[0], router.num_topk
+    idx = torch.empty((T, k), dtype=torch.int64, device=logits.device)
+    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    ep_route(router, logits, bias, idx, w, stream)
+    return idx, w
+
+
+def route_backward(grad_topk_w, logits, topk_idx, router, stream=None):
+    """Gradient over the logits of route's weights."""
+    g = torch.empty_like(logits)
+    ep_route_backward(router, logits, topk_idx, grad_topk_w, g, stream)
+    return g
+
+
+def expert_gemm(expert_offset, a, a_scales, w, w_scales, num_ranks=1, rank_capacity=0, stream=None):
+    """bf16 rows [rows, N]; rows of no segment hold whatever the allocation held."""
+    out = torch.empty((a.shape[0], w.shape[1]), dtype=torch.bfloat16, device=a.device)
+    ep_expert_gemm(expert_offset, a, a_scales, w, w_scales, out, num_ranks, rank_capacity, stream)
+    return out
+
+
+def expert_gated(expert_offset, a, a_scales, w, w_scales, num_ranks=1, rank_capacity=0, stream=None):
+    """FP8_S128 rows: e4m3 [rows, N] and scales [rows, N/128]; rows of no segment as the allocation held them."""
+    N = w.shape[1] // 2
+    q = torch.empty((a.shape[0], N), dtype=torch.uint8, device=a.device)
+    s = torch.empty((a.shape[0], N // 128), dtype=torch.float32, device=a.device)
+    ep_expert_gated(expert_offset, a, a_scales, w, w_scales, q, s, num_ranks, rank_capacity, stream)
+    return q, s
+
+
+def combine_backward(dy, expert_out, handle: Handle, stream=None):
+    """Returns grad_expert_out [rows, H] bf16 (rows of no slot as the allocation held them) and grad_topk_w [T, k]."""
+    g = torch.empty_like(expert_out)
+    gw = torch.empty_like(handle.topk_w)
+    ep_combine_backward(handle.shape, dy, expert_out, handle.token_slot, handle.topk_w, g, gw, stream)
+    return g, gw

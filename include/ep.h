@@ -445,6 +445,142 @@ int ep_expert_requant_mxfp8(const ep_shape *shape, const int32_t *expert_offset,
                             const float *factor, const uint8_t *recv_q, const float *recv_scales,
                             uint8_t *out_q, uint8_t *out_e8m0, void *stream);
 
+/* ---- the router -------------------------------------------------------------- */
+
+/* How a token's experts are chosen from its logits z [E].  Supported range
+ * (else EP_EINVAL): 1 <= num_experts <= 4096; 1 <= num_topk <= 32, <=
+ * num_experts; 1 <= num_groups <= 64, num_experts % num_groups == 0; 1 <=
+ * topk_groups <= num_groups; group_top 1 or 2, and at most the experts of a
+ * group where there are groups; topk_groups * (experts of a group) >=
+ * num_topk; scale finite. */
+enum ep_score {
+    EP_SCORE_SOFTMAX = 0,   /* p = softmax(z) over the token's experts */
+    EP_SCORE_SIGMOID = 1    /* p = 1 / (1 + exp(-z)) */
+};
+typedef struct ep_router {
+    int32_t num_experts;  /* E */
+    int32_t num_topk;     /* k */
+    int32_t score;        /* EP_SCORE_SOFTMAX | EP_SCORE_SIGMOID */
+    int32_t num_groups;   /* G: experts [g E/G, (g+1) E/G) form group g; 1: no groups */
+    int32_t topk_groups;  /* groups that stay */
+    int32_t group_top;    /* keys summed for a group's mark: its largest, or its two largest */
+    int32_t renormalize;  /* 1: the taken scores are divided by their sum */
+    int32_t logits_bf16;  /* 1: logits (and their gradient) are bf16, 0: fp32 */
+    float scale;          /* factor of every weight */
+} ep_router;
+
+/*
+ * Routing: the experts and weights that the layout and the dispatch take.
+ *     key[e] = p[e] + bias[e]   (p[e] without a bias); -inf where z[e] is -inf
+ *              or NaN, or where the key is NaN: such an expert is never taken
+ *     with groups: a group's mark is the sum of its group_top largest keys
+ *              (-inf where that sum is NaN); the topk_groups groups with the
+ *              largest marks stay, the others' keys become -inf
+ *     topk_idx[t, j] = the expert with the j-th largest key, ties to the
+ *              lowest index (groups too); -1 where no key above -inf is left
+ *     topk_w[t, j] = scale * p[e_j], or scale * p[e_j] / sum_i p[e_i] over the
+ *              taken experts with renormalize (0 where that sum is 0); 0 for a
+ *              slot that is -1
+ * The bias steers the choice only (load balance): it is not in the weights and
+ * has no gradient.  A row whose logits are all -inf (a padded token) gets -1 in
+ * every slot, which the layout and the dispatch skip.  Experts at +inf share a
+ * softmax evenly.  Scores, keys and sums are binary64 and the weights are
+ * rounded once, so the choice is that of the binary64 scores.
+ *   logits [T, E] fp32 or bf16; bias [E] fp32 or NULL
+ *   topk_idx [T, k] int64; topk_w [T, k] fp32
+ * 0 <= num_tokens, num_tokens * num_topk < 2^31.
+ */
+int ep_route(const ep_router *router, int64_t num_tokens, const void *logits, const float *bias,
+             int64_t *topk_idx, float *topk_w, void *stream);
+
+/*
+ * Gradient of ep_route's weights over its logits, with the choice held fixed:
+ * grad_logits[t, e] = sum_j grad_topk_w[t, j] d topk_w[t, j] / d z[t, e],
+ * computed in binary64 from the logits again and rounded once.  A slot whose
+ * topk_idx is negative (or >= E) adds nothing; an index that occurs twice in a
+ * row counts twice.  Every element is written: 0 for experts that were not
+ * taken, except under a softmax without renormalize, where every expert has a
+ * gradient.
+ *   logits [T, E] as for ep_route; topk_idx [T, k] from ep_route;
+ *   grad_topk_w [T, k] fp32; grad_logits [T, E] of the logits' type
+ */
+int ep_route_backward(const ep_router *router, int64_t num_tokens, const void *logits,
+                      const int64_t *topk_idx, const float *grad_topk_w, void *grad_logits, void *stream);
+
+/* ---- the experts' products over fp8 rows ----------------------------------- */
+
+/* Shapes of one grouped product.  Supported range (else EP_EINVAL): 0 <= rows
+ * < 2^30; 1 <= num_experts <= 4096; in_features a multiple of 128;
+ * out_features a multiple of 8 (ep_expert_gated: of 128); both at most 2^20;
+ * 1 <= num_ranks <= 64 dividing num_experts; rank_capacity 0 or rows /
+ * num_ranks exactly. */
+typedef struct ep_expert_shape {
+    int64_t rows;           /* receive rows: the capacity of a and of the output */
+    int32_t num_experts;    /* E: expert_offset has E + 1 entries */
+    int32_t in_features;    /* K */
+    int32_t out_features;   /* N: width of the output rows */
+    int32_t num_ranks;      /* R: used with rank_capacity only */
+    int32_t rank_capacity;  /* 0: expert e's rows are [expert_offset[e], expert_offset[e+1]);
+                               M > 0: RANK_MAJOR, they lie in the block of rank e / (E/R) as
+                               ep_dispatch places them (those past the block were dropped) */
+} ep_expert_shape;
+
+/*
+ * Each expert's rows times its weights (the expert stage between dispatch and
+ * combine), both in e4m3 with block scales:
+ *     out[s, n] = bf16_rne(sum_b a_scales[s, b] * w_scales[e, n / 128, b]
+ *                          * sum_{i < 128} a[s, 128 b + i] * w[e, n, 128 b + i])
+ * with fp32 accumulation, b ascending over the K / 128 blocks (in a few parts
+ * that are added at the end where that fills the chip).  e is the expert whose
+ * segment holds row s; rows of no segment are neither read nor written, and
+ * experts without rows cost no weight traffic.  expert_offset stays on the
+ * device: no count reaches the host.  It may also be a slice [e0 .. e1] of a
+ * dispatch's expert_offset with the weights of those experts (one rank's
+ * share); row numbers stay absolute.
+ *   expert_offset [E+1] int32, ascending; entries are clamped to [0, rows]
+ *   a        [rows, K] e4m3, a_scales [rows, K/128] fp32: FP8_S128 rows, as
+ *            ep_dispatch delivers or ep_quant_fp8_s128 makes them
+ *   w        [E, N, K] e4m3, w_scales [E, ceil(N/128), K/128] fp32
+ *   out      [rows, N] bf16: what ep_combine takes with y_format BF16
+ * a, w and out are 16-byte aligned.
+ */
+int ep_expert_gemm(const ep_expert_shape *shape, const int32_t *expert_offset, const uint8_t *a,
+                   const float *a_scales, const uint8_t *w, const float *w_scales, uint16_t *out,
+                   void *stream);
+
+/*
+ * The gated first half of an expert: with g and u the products (as above, kept
+ * in fp32) of a row with the expert's gate and up weights,
+ *     h[s, n] = g / (1 + exp(-g)) * u
+ * leaves as FP8_S128 rows by ep_quant_fp8_s128's rule on the fp32 values (per
+ * 128 elements scale = amax / 448, 1 for an all-zero group; e4m3_rne_sat(h /
+ * scale)): the next ep_expert_gemm takes them as they are.
+ *   w        [E, 2 N, K] e4m3: N gate rows, then N up rows;
+ *   w_scales [E, 2 N / 128, K/128] fp32
+ *   out_q    [rows, N] e4m3 (16-byte aligned), out_scales [rows, N/128] fp32
+ */
+int ep_expert_gated(const ep_expert_shape *shape, const int32_t *expert_offset, const uint8_t *a,
+                    const float *a_scales, const uint8_t *w, const float *w_scales, uint8_t *out_q,
+                    float *out_scales, void *stream);
+
+/* ---- the combine's backward pass -------------------------------------------- */
+
+/*
+ * Gradients of ep_combine (y_format BF16) from the gradient dy of its result:
+ *     grad_expert_out[s, h] = bf16_rne(topk_w[t,j] * dy[t,h]), s = token_slot[t,j]
+ *     grad_topk_w[t, j]     = sum_h dy[t,h] * expert_out[s, h]   (fp32)
+ * A slot outside [0, rows) is masked: its weight's gradient is 0.  Rows that no
+ * slot names are left untouched.  The slots of a dispatch's handle are
+ * distinct; a row that two slots name gets one of the two gradients.
+ * (The dispatch's own backward pass is ep_combine with weights 1; that of
+ * ep_combine_ranks is ep_dispatch_ranks_cached of dy.)
+ *   dy [T, H] bf16; expert_out, grad_expert_out [rows, H] bf16; all 16-byte
+ *   aligned; token_slot, topk_w, grad_topk_w [T, k]; rows as in ep_combine
+ */
+int ep_combine_backward(const ep_shape *shape, const uint16_t *dy, const uint16_t *expert_out,
+                        const int32_t *token_slot, const float *topk_w, uint16_t *grad_expert_out,
+                        float *grad_topk_w, void *stream);
+
 /* ---- accounting (host arithmetic on host copies of the layout counts) ---- */
 
 /* [MORI] "Bandwidth Computation": RDMA algo tokens are the layout's (token,

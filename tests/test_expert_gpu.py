@@ -1,0 +1,208 @@
+"""The experts' products on the GPU against the 64-bit implementation, at
+sizes, segments and layouts where they can go wrong.  Rows of no segment must
+stay as they were."""
+import numpy as np
+import pytest
+
+import moe_ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def ep():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from combine_dispatch_layout_02_amd import ep as mod
+    mod.load()
+    return mod
+
+
+def _draw(rng, rows, E, K, wide, sigma=100.0):
+    """Random rows and weights; every e4m3 value but NaN occurs."""
+    def q(*shape):
+        x = torch.from_numpy((rng.standard_normal(shape) * sigma).astype(np.float32)).clamp(-448, 448)
+        return x.to(torch.float8_e4m3fn).view(torch.uint8)
+    a, w = q(rows, K), q(E, wide, K)
+    a_s = torch.from_numpy((rng.uniform(0.5, 2.0, (rows, K // 128)) / sigma).astype(np.float32))
+    w_s = torch.from_numpy((rng.uniform(0.5, 2.0, (E, (wide + 127) // 128, K // 128))
+                            / (sigma * np.sqrt(K))).astype(np.float32))
+    return a, a_s, w, w_s
+
+
+def _np(*ts):
+    return [t.numpy() for t in ts]
+
+
+def _check_product(ep, offset, a, a_s, w, w_s, R=1, M=0):
+    off = torch.tensor(offset, dtype=torch.int32)
+    y = torch.full((a.shape[0], w.shape[1]), 7.0, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_gemm(off.cuda(), a.cuda(), a_s.cuda(), w.cuda(), w_s.cuda(), y, R, M)
+    ref, mag, valid = moe_ref.product(offset, *_np(a, a_s, w, w_s), R, M)
+    err = moe_ref.sum_error(mag, a.shape[1])
+    got = y.cpu().double().numpy()
+    bad = np.abs(got - ref) > moe_ref.BF16_HALF * (np.abs(ref) + err) + err
+    assert not bad[valid].any(), np.argwhere(bad & valid[:, None])[:5]
+    assert (got[~valid] == 7.0).all()
+    return y
+
+
+def _check_gated(ep, offset, a, a_s, w, w_s, R=1, M=0):
+    off = torch.tensor(offset, dtype=torch.int32)
+    N = w.shape[1] // 2
+    q = torch.full((a.shape[0], N), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((a.shape[0], N // 128), 7.0, device="cuda")
+    ep.ep_expert_gated(off.cuda(), a.cuda(), a_s.cuda(), w.cuda(), w_s.cuda(), q, s, R, M)
+    h, err, valid = moe_ref.gated(offset, *_np(a, a_s, w, w_s), R, M)
+    qn, sn = q.cpu().numpy(), s.cpu().numpy()
+    moe_ref.check_quantised(qn, sn, h, err, valid)
+    assert (qn[~valid] == 0x55).all() and (sn[~valid] == 7.0).all()
+    return q, s
+
+
+def _offsets(counts, first=0):
+    return [first] + (first + np.cumsum(counts)).tolist()
+
+
+# experts' row counts: none, one, ends at, before and after tile borders, long ones
+COUNTS = [
+    [1], [16], [0, 1], [3, 0, 5], [15, 16, 17], [31, 32, 33, 0, 1], [63, 64, 65], [127, 0, 128, 129], [300, 2, 0, 0, 1],
+    [255, 257], [8] * 40, [0] * 20 + [5] + [0] * 20, [700],
+]
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: "-".join(map(str, c[:5])) + f"x{len(c)}")
+@pytest.mark.parametrize("K,N", [(128, 8), (256, 136), (640, 256), (1152, 1000)])
+def test_product_segments(ep, counts, K, N):
+    rng = np.random.default_rng(K + N + len(counts))
+    off = _offsets(counts)
+    _check_product(ep, off, *_draw(rng, off[-1] + 9, len(counts), K, N))
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: "-".join(map(str, c[:5])) + f"x{len(c)}")
+@pytest.mark.parametrize("K,N", [(128, 128), (384, 256), (1152, 384)])
+def test_gated_segments(ep, counts, K, N):
+    rng = np.random.default_rng(K + N + len(counts))
+    off = _offsets(counts)
+    _check_gated(ep, off, *_draw(rng, off[-1] + 9, len(counts), K, 2 * N))
+
+
+@pytest.mark.parametrize("rows,E,K,N", [(5000, 3, 512, 520), (2600, 64, 256, 264), (4100, 1, 1024, 384),
+                                        (1, 1, 7168, 2048), (8, 300, 256, 128), (2048, 4096, 128, 128),
+                                        (1100, 2, 2048, 640)])
+def test_random_segments(ep, rows, E, K, N):
+    """Random segments of every mean length, some rows before the first and behind the last segment."""
+    rng = np.random.default_rng(rows + E)
+    cut = np.sort(rng.integers(rows // 50, rows - rows // 60 + 1, size=E + 1)).tolist()
+    if E > 100:
+        N = min(N, 128)
+    a, a_s, w, w_s = _draw(rng, rows, E, K, N)
+    _check_product(ep, cut, a, a_s, w, w_s)
+    N = (N + 127) // 128 * 128
+    _check_gated(ep, cut, *_draw(rng, rows, E, K, 2 * N if E <= 100 else 256))
+
+
+@pytest.mark.parametrize("E,R,M,counts", [(4, 2, 40, [3, 20, 17, 9]), (6, 3, 16, [16, 0, 20, 5, 0, 0]),
+                                          (8, 4, 130, [1, 200, 100, 30, 0, 0, 65, 65]), (2, 1, 33, [30, 30])])
+def test_rank_major_rows(ep, E, R, M, counts):
+    """RANK_MAJOR blocks, some with more rows than they hold."""
+    rng = np.random.default_rng(M)
+    off = _offsets(counts)
+    _check_product(ep, off, *_draw(rng, R * M, E, 256, 200), R, M)
+    _check_gated(ep, off, *_draw(rng, R * M, E, 256, 256), R, M)
+
+
+def test_slice_of_the_offsets(ep):
+    """One rank's experts: a slice of a dispatch's offsets with those experts' weights."""
+    rng = np.random.default_rng(6)
+    off = _offsets([30, 5, 0, 70, 12, 9])
+    a, a_s, w, w_s = _draw(rng, off[-1], 6, 384, 256)
+    whole = _check_product(ep, off, a, a_s, w, w_s)
+    part = _check_product(ep, off[2:5], a, a_s, w[2:4], w_s[2:4])
+    lo, hi = off[2], off[4]
+    assert torch.equal(part[lo:hi], whole[lo:hi])
+
+
+def test_offsets_out_of_range_are_clamped(ep):
+    """Entries below 0, past the rows or descending reach no row outside the buffers."""
+    rng = np.random.default_rng(7)
+    a, a_s, w, w_s = _draw(rng, 50, 4, 256, 256)
+    for bad in ([-5, 10, 20, 30, 90], [0, 60, 70, 80, 90], [40, 30, 20, 10, 0], [0, 10, 5, 60, 20]):
+        y = torch.full((50 + 64, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+        ep.ep_expert_gemm(torch.tensor(bad, dtype=torch.int32, device="cuda"), a.cuda(), a_s.cuda(), w.cuda(),
+                          w_s.cuda(), y[:50])
+        assert (y[50:] == 7.0).all()
+    y = torch.full((50, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_gemm(torch.zeros(5, dtype=torch.int32, device="cuda"), a.cuda(), a_s.cuda(), w.cuda(), w_s.cuda(), y)
+    assert (y == 7.0).all()
+    none = torch.empty(0, 256, dtype=torch.uint8, device="cuda")
+    assert ep.expert_gemm(torch.zeros(5, dtype=torch.int32, device="cuda"), none,
+                          torch.empty(0, 2, device="cuda"), w.cuda(), w_s.cuda()).shape == (0, 256)
+
+
+def test_nan_rows_stay_in_their_rows(ep):
+    """NaN in a row, and in the rows around a segment, reaches that row only; inf and zero scales follow fp32."""
+    rng = np.random.default_rng(9)
+    off = [4, 20, 41]
+    a, a_s, w, w_s = _draw(rng, 60, 2, 256, 256)
+    ref = _check_product(ep, off, a, a_s, w, w_s)
+    a[:4], a[41:] = 0x7F, 0x7F
+    a_s[:4], a_s[41:] = float("nan"), float("inf")
+    a[10, 3], a_s[30, 1] = 0x7F, float("nan")
+    y = ep.expert_gemm(torch.tensor(off, dtype=torch.int32).cuda(), a.cuda(), a_s.cuda(), w.cuda(), w_s.cuda())
+    q, s = ep.expert_gated(torch.tensor(off, dtype=torch.int32).cuda(), a.cuda(), a_s.cuda(), w.cuda(), w_s.cuda())
+    keep = [r for r in range(4, 41) if r not in (10, 30)]
+    assert torch.equal(y[keep], ref[keep])
+    assert torch.isnan(y[[10, 30]]).all() and not torch.isnan(s[keep]).any()
+    assert ((q[[10, 30]] & 0x7F) == 0x7F).all()
+
+
+def test_all_zero_groups_and_saturation(ep):
+    """Groups of zeros get the scale 1; gates at both ends of the exponential."""
+    rng = np.random.default_rng(10)
+    a, a_s, w, w_s = _draw(rng, 40, 1, 256, 512)
+    a[7] = 0
+    w[0, 256:384] = 0             # the up rows of the first group
+    a_s[9] *= 1e6                 # gates of +- thousands: h = g u or 0
+    a_s[11] *= 1e-6
+    q, s = _check_gated(ep, [0, 40], a, a_s, w, w_s)
+    assert (s[:, 0] == 1).all() and (q[:, :128] & 0x7F == 0).all() and (s[7] == 1).all()
+
+
+def test_products_repeat_to_the_bit(ep):
+    rng = np.random.default_rng(12)
+    off = torch.tensor(_offsets([200, 3, 0, 90]), dtype=torch.int32).cuda()
+    x = [t.cuda() for t in _draw(rng, 293, 4, 2048, 512)]
+    y, (q, s) = ep.expert_gemm(off, *x), ep.expert_gated(off, *x)
+    for _ in range(5):
+        assert torch.equal(ep.expert_gemm(off, *x), y)
+        q2, s2 = ep.expert_gated(off, *x)
+        assert torch.equal(q2, q) and torch.equal(s2, s)
+
+
+@pytest.mark.parametrize("counts,K,N", [([1] * 8, 2048, 7168), ([150, 90], 7168, 1024), ([40, 1, 200], 2048, 2048)])
+def test_wide_layers(ep, counts, K, N):
+    rng = np.random.default_rng(K)
+    off = _offsets(counts)
+    _check_product(ep, off, *_draw(rng, off[-1] + 3, len(counts), K, N))
+    _check_gated(ep, off, *_draw(rng, off[-1] + 3, len(counts), K, 2 * (N // 4)))
+
+
+def test_weights_past_two_gib(ep):
+    """An expert whose weights start past 2^31 and 2^32 bytes."""
+    E, N, K = 5, 32768, 32768     # 1 GiB an expert
+    rng = np.random.default_rng(13)
+    w = torch.zeros(E, N, K, dtype=torch.uint8, device="cuda")
+    a, a_s, _, _ = _draw(rng, 6, 1, K, 8)
+    last = torch.from_numpy((rng.standard_normal((256, K)) * 100).astype(np.float32)).clamp(-448, 448)
+    last = last.to(torch.float8_e4m3fn).view(torch.uint8)
+    w[E - 1, -256:] = last.cuda()
+    w_s = torch.full((E, N // 128, K // 128), 1e-5, device="cuda")
+    y = ep.expert_gemm(torch.tensor([0, 0, 0, 2, 2, 6], dtype=torch.int32).cuda(), a.cuda(), a_s.cuda(), w, w_s)
+    ref, mag, _ = moe_ref.product([0, 6], a.numpy(), a_s.numpy(), last.numpy()[None],
+                                  np.full((1, 2, K // 128), 1e-5, np.float32))
+    err = moe_ref.sum_error(mag, K)
+    got = y.cpu().double().numpy()
+    assert (got[:, :-256] == 0).all() and (got[:2] == 0).all()
+    assert (np.abs(got[2:, -256:] - ref[2:]) <= moe_ref.BF16_HALF * (np.abs(ref[2:]) + err[2:]) + err[2:]).all()

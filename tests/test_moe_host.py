@@ -1,0 +1,203 @@
+"""The router, the experts' products and the combine's backward pass on the
+host (no GPU): every argument error is found before anything is enqueued, an
+empty call succeeds without touching a pointer, and the Python layer refuses
+wrong dtypes, shapes and devices.  The 64-bit implementations the GPU tests
+compare with are checked here against differences and torch."""
+import ctypes
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import moe_ref
+from combine_dispatch_layout_02_amd import ep
+
+P = ctypes.c_void_p
+FAKE, ODD = P(0x1000), P(0x1008)   # never dereferenced: the host checks come first
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return ep.load()
+
+
+GOOD = dict(E=256, k=8, score="sigmoid", num_groups=8, topk_groups=4, group_top=2, renormalize=True, scale=2.5)
+
+
+def _router(**kw):
+    d = dict(GOOD, **kw)
+    raw = d.pop("raw", {})
+    r = ep.make_router(d.pop("E"), d.pop("k"), d.pop("score"), **d)
+    for name, v in raw.items():
+        setattr(r, name, v)
+    return r
+
+
+@pytest.mark.parametrize("bad", [
+    dict(E=0, num_groups=1, topk_groups=1), dict(E=4097, num_groups=1, topk_groups=1), dict(k=0), dict(k=33),
+    dict(E=16, k=17, num_groups=1, topk_groups=1), dict(num_groups=0, topk_groups=1), dict(num_groups=3),
+    dict(num_groups=128, topk_groups=128), dict(topk_groups=0), dict(topk_groups=9), dict(group_top=0),
+    dict(group_top=3), dict(E=8, k=2, num_groups=8, topk_groups=4, group_top=2),
+    dict(E=16, k=8, num_groups=8, topk_groups=3, group_top=1), dict(scale=float("inf")), dict(scale=float("nan")),
+    dict(raw=dict(score=2)), dict(raw=dict(score=-1)), dict(raw=dict(renormalize=2)), dict(raw=dict(logits_bf16=2))])
+def test_router_refuses(lib, bad):
+    r = _router(**bad)
+    assert lib.ep_route(ctypes.byref(r), 4, FAKE, None, FAKE, FAKE, None) == ep.EP_EINVAL
+    assert lib.ep_route_backward(ctypes.byref(r), 4, FAKE, FAKE, FAKE, FAKE, None) == ep.EP_EINVAL
+
+
+def test_router_arguments(lib):
+    r = _router()
+    byref = ctypes.byref(r)
+    assert lib.ep_route(None, 4, FAKE, None, FAKE, FAKE, None) == ep.EP_EINVAL
+    assert lib.ep_route(byref, -1, FAKE, None, FAKE, FAKE, None) == ep.EP_EINVAL
+    assert lib.ep_route(byref, 2 ** 28, FAKE, None, FAKE, FAKE, None) == ep.EP_EINVAL   # T * k = 2^31
+    assert lib.ep_route(byref, 0, None, None, None, None, None) == ep.EP_OK
+    assert lib.ep_route_backward(byref, 0, None, None, None, None, None) == ep.EP_OK
+    for i in (0, 2, 3):
+        args = [FAKE, FAKE, FAKE, FAKE]
+        args[i] = None
+        assert lib.ep_route(byref, 4, *args, None) == ep.EP_EINVAL
+    for i in range(4):
+        args = [FAKE] * 4
+        args[i] = None
+        assert lib.ep_route_backward(byref, 4, *args, None) == ep.EP_EINVAL
+    with pytest.raises(ValueError):
+        ep.make_router(16, 2, "relu")
+
+
+def _expert(rows=64, E=4, K=256, N=256, R=1, M=0):
+    return ep.ep_expert_shape(rows, E, K, N, R, M)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(rows=-1), dict(rows=2 ** 30), dict(E=0), dict(E=4097), dict(K=0), dict(K=64), dict(K=192), dict(K=2 ** 20 + 128),
+    dict(N=0), dict(N=12), dict(N=2 ** 20 + 128), dict(R=0), dict(R=3), dict(R=65, E=130), dict(M=-1),
+    dict(R=2, M=31), dict(R=2, M=33)])
+def test_expert_shapes_refused(lib, bad):
+    sh = _expert(**bad)
+    for fn, outs in ((lib.ep_expert_gemm, [FAKE]), (lib.ep_expert_gated, [FAKE, FAKE])):
+        assert fn(ctypes.byref(sh), *[FAKE] * 5, *outs, None) == ep.EP_EINVAL
+
+
+def test_expert_arguments(lib):
+    for fn, outs in ((lib.ep_expert_gemm, 1), (lib.ep_expert_gated, 2)):
+        sh = _expert()
+        assert fn(None, *[FAKE] * (5 + outs), None) == ep.EP_EINVAL
+        empty = _expert(rows=0)
+        assert fn(ctypes.byref(empty), *[None] * (5 + outs), None) == ep.EP_OK
+        for i in range(5 + outs):
+            args = [FAKE] * (5 + outs)
+            args[i] = None
+            assert fn(ctypes.byref(sh), *args, None) == ep.EP_EINVAL
+        for i in (1, 3, 5):   # a, w, out
+            args = [FAKE] * (5 + outs)
+            args[i] = ODD
+            assert fn(ctypes.byref(sh), *args, None) == ep.EP_EALIGN
+    assert lib.ep_expert_gated(ctypes.byref(_expert(N=264)), *[FAKE] * 7, None) == ep.EP_EINVAL   # N % 128
+    assert lib.ep_expert_gemm(ctypes.byref(_expert(N=264)), *[FAKE] * 5, ODD, None) == ep.EP_EALIGN
+
+
+def test_combine_backward_arguments(lib):
+    sh = ep.make_shape(64, 256, 16, 4, 1, 2)
+    byref = ctypes.byref(sh)
+    fn = lib.ep_combine_backward
+    assert fn(None, *[FAKE] * 6, None) == ep.EP_EINVAL
+    assert fn(ctypes.byref(ep.make_shape(64, 250, 16, 4, 1, 2)), *[FAKE] * 6, None) == ep.EP_EINVAL
+    for fmt in (ep.EP_FMT_MXFP8, ep.EP_FMT_NVFP4):
+        assert fn(ctypes.byref(ep.make_shape(64, 256, 16, 4, 1, 2, 0, fmt)), *[FAKE] * 6, None) == ep.EP_EINVAL
+    assert fn(ctypes.byref(ep.make_shape(0, 256, 16, 4, 1, 2)), *[None] * 6, None) == ep.EP_OK
+    for i in range(6):
+        args = [FAKE] * 6
+        args[i] = None
+        assert fn(byref, *args, None) == ep.EP_EINVAL
+    for i in (0, 1, 4):
+        args = [FAKE] * 6
+        args[i] = ODD
+        assert fn(byref, *args, None) == ep.EP_EALIGN
+
+
+def test_python_layer_refuses():
+    f32, bf, u8, i32, i64 = torch.float32, torch.bfloat16, torch.uint8, torch.int32, torch.int64
+    z = lambda *s, d=f32: torch.zeros(*s, dtype=d)  # noqa: E731
+    r = ep.make_router(16, 2)
+    good = dict(logits=z(4, 16), bias=None, topk_idx=z(4, 2, d=i64), topk_w=z(4, 2))
+    for bad in (dict(logits=z(4, 16, d=torch.float16)), dict(logits=z(4, 8)), dict(logits=z(64)), dict(bias=z(8)),
+                dict(bias=z(16, d=bf)), dict(topk_idx=z(4, 2, d=i32)), dict(topk_w=z(4, 3)), dict(topk_w=z(3, 2)), {}):
+        with pytest.raises(ValueError):   # {}: tensors of the host
+            ep.ep_route(r, **dict(good, **bad))
+    back = dict(logits=z(4, 16), topk_idx=z(4, 2, d=i64), grad_topk_w=z(4, 2), grad_logits=z(4, 16))
+    for bad in (dict(grad_logits=z(4, 16, d=bf)), dict(grad_topk_w=z(4, 2, d=bf)), dict(topk_idx=z(4, 1, d=i64)), {}):
+        with pytest.raises(ValueError):
+            ep.ep_route_backward(r, **dict(back, **bad))
+    x = dict(expert_offset=z(4, d=i32), a=z(6, 256, d=u8), a_scales=z(6, 2), w=z(3, 256, 256, d=u8), w_scales=z(3, 2, 2))
+    outs = {ep.ep_expert_gemm: dict(out=z(6, 256, d=bf)),
+            ep.ep_expert_gated: dict(out_q=z(6, 128, d=u8), out_scales=z(6, 1))}
+    for fn, out in outs.items():
+        for bad in (dict(expert_offset=z(3, d=i32)), dict(expert_offset=z(4, d=i64)), dict(a=z(6, 200, d=u8)),
+                    dict(a=z(6, 256)), dict(a_scales=z(6, 4)), dict(w=z(3, 256, 128, d=u8)), dict(w=z(256, 256, d=u8)),
+                    dict(w_scales=z(3, 1, 2)), dict(w_scales=z(3, 2, 2, d=bf)), {}):
+            with pytest.raises((ValueError, IndexError)):
+                fn(**{**x, **out, **bad})
+    with pytest.raises(ValueError):
+        ep.ep_expert_gated(**{**x, "w": z(3, 128, 256, d=u8), "w_scales": z(3, 1, 2)}, **outs[ep.ep_expert_gated])
+    with pytest.raises(ValueError):
+        ep.ep_expert_gemm(**x, out=z(6, 256))
+    with pytest.raises(ValueError):
+        ep.ep_expert_gated(**x, out_q=z(6, 256, d=u8), out_scales=z(6, 1))
+    sh = ep.make_shape(4, 16, 16, 1, 1, 2)
+    c = dict(dy=z(4, 16, d=bf), expert_out=z(8, 16, d=bf), token_slot=z(4, 2, d=i32), topk_w=z(4, 2),
+             grad_expert_out=z(8, 16, d=bf), grad_topk_w=z(4, 2))
+    for bad in (dict(dy=z(4, 16)), dict(expert_out=z(4, 16, d=bf)), dict(token_slot=z(4, 2, d=i64)),
+                dict(topk_w=z(4, 2, d=bf)), dict(grad_expert_out=z(8, 16)), dict(grad_topk_w=z(8, 2)), {}):
+        with pytest.raises(ValueError):
+            ep.ep_combine_backward(sh, **dict(c, **bad))
+
+
+@pytest.mark.parametrize("score,renorm", itertools.product(("softmax", "sigmoid"), (False, True)))
+def test_reference_gradient_against_differences(score, renorm):
+    """The Jacobian the GPU gradient is compared with, against differences of the 64-bit weights."""
+    rng = np.random.default_rng(3)
+    z = rng.standard_normal((5, 9))
+    z[1, 4] = -np.inf
+    idx, _ = moe_ref.route(z, 4, score, renorm=renorm, scale=1.5)
+    idx[2, 3] = idx[2, 0]      # an index twice, and a masked slot
+    idx[3, 1] = -1
+    g = rng.standard_normal((5, 4))
+    got = moe_ref.route_backward(z, idx, g, score, renorm, 1.5)
+
+    def loss(zz, t):
+        live = [j for j in range(4) if idx[t, j] >= 0]
+        return float(np.dot(g[t, live], moe_ref.weights(zz, [int(idx[t, j]) for j in live], score, renorm, 1.5)))
+    h = 1e-5
+    for t in range(5):
+        for e in range(9):
+            if not np.isfinite(z[t, e]):
+                assert got[t, e] == 0
+                continue
+            a, b = z[t].copy(), z[t].copy()
+            a[e] += h
+            b[e] -= h
+            # truncation h^2 / 6 times a third derivative below 2 |g|_1, and 64-bit rounding over 2 h
+            assert abs((loss(a, t) - loss(b, t)) / (2 * h) - got[t, e]) < 1e-9
+
+
+def test_reference_route_against_torch():
+    rng = np.random.default_rng(5)
+    z = rng.standard_normal((50, 24))
+    zt = torch.from_numpy(z)
+    for score, renorm in itertools.product(("softmax", "sigmoid"), (False, True)):
+        p = torch.softmax(zt, 1) if score == "softmax" else torch.sigmoid(zt)
+        v, i = p.topk(5, 1)
+        if renorm:
+            v = v / v.sum(1, keepdim=True)
+        idx, w = moe_ref.route(z, 5, score, renorm=renorm, scale=2.0)
+        np.testing.assert_array_equal(idx, i.numpy())
+        np.testing.assert_allclose(w, 2.0 * v.numpy(), rtol=1e-12)
+
+
+def test_reference_e4m3_against_torch():
+    b = np.arange(256, dtype=np.uint8)
+    want = torch.from_numpy(b).view(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(moe_ref.e4m3_value(b), want)
