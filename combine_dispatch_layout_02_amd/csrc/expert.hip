@@ -199,6 +199,215 @@ __global__ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
     }
 }
 
+// ---------------------------------------------------------------- many rows
+
+constexpr int kTileThreads = 512, kTileN = 256;   // 8 waves; weight rows of a tile
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+// Buffers of at most 2^31 bytes from a wave-uniform base: a load is then one
+// 32-bit register of offset per lane and a scalar one per block of K.
+__device__ __forceinline__ rsrc_t buffer(const void *p) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7FFFFFFF, 0x00020000);
+}
+
+// 16 bytes per lane from memory into LDS at base + 16 lane, without a register.
+__device__ __forceinline__ void load_to_lds(rsrc_t b, uint8_t *lds, uint32_t off, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void *)lds, 16, (int)off, (int)soff,
+                                             0, 0);
+}
+
+__device__ __forceinline__ float load_f32(rsrc_t b, uint32_t off, uint32_t soff) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, (int)soff, 0));
+}
+
+// A lane's 32 bytes of a row of a tile in LDS, given where its two pieces lie.
+// Rows are 128 bytes, and their 16-byte pieces are permuted by the row (piece c
+// lies at c ^ (r % 8)), so that the 8 lanes of one LDS cycle touch every bank
+// once; rows 16 apart have the same permutation.
+__device__ __forceinline__ i32x8 lds_operand(const uint8_t *lo16, const uint8_t *hi16) {
+    const vec16 lo = ld16(lo16), hi = ld16(hi16);
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// One block: BM rows by 256 weight rows (gated: 128 gate rows and the matching
+// 128 up rows), 8 waves, WN of them side by side.  Both operands of a block of
+// K = 128 are staged in LDS, two buffers in turn: the next block's loads are
+// in flight while this one is multiplied.
+template <int BM, int WN, bool GATED>
+__global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
+    ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
+    uint16_t *out, uint8_t *oq, float *oqs, int slots, int cols) {
+    constexpr int WM = 8 / WN, NF = kTileN / WN / 16, MF = BM / WM / 16;
+    constexpr int HALF = GATED ? 2 : 1;            // gate and up, or one product
+    constexpr int WCOLS = kTileN / HALF / WN;      // columns of the result per wave
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[(kTileN + BM) * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[(kTileN + BM) * 128];
+    __shared__ int found;
+    __shared__ float amax[GATED ? WN : 1][GATED ? BM : 1];
+
+    const int per = 8 * cols, sb = blockIdx.x / per, in = blockIdx.x % per;
+    const int slot = sb * 8 + in % 8, ct = in / 8;
+    if (slot >= slots) return;
+    int e, row, end;
+    if (!find_tile(off, s, slot, BM, &found, &e, &row, &end)) return;
+
+    const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wn = wid % WN, wm = wid / WN;
+    const int r16 = lane & 15, quad = lane >> 4;
+    const int KB = s.K / 128;
+    const int wrows = HALF * s.N;
+    const int n0 = ct * (kTileN / HALF);           // first column of the result
+    const uint8_t *we = w + (size_t)e * wrows * s.K;
+    const float *wse = ws + (size_t)e * ((wrows + 127) / 128) * KB;
+
+    // staging: pass p of the block covers 64 rows, a wave 8 of them
+    const int srow = wid * 8 + (lane >> 3);                    // + 64 p
+    const uint32_t piece = (uint32_t)(((lane & 7) ^ (srow & 7)) << 4);
+    uint32_t woff[kTileN / 64], xoff[BM / 64];
+#pragma unroll
+    for (int p = 0; p < kTileN / 64; ++p) {
+        const int r = srow + 64 * p;
+        const int n = GATED ? r % 128 : min(r, wrows - 1 - n0);
+        woff[p] = (uint32_t)n * (uint32_t)s.K + piece;
+    }
+#pragma unroll
+    for (int p = 0; p < BM / 64; ++p)
+        xoff[p] = (uint32_t)min(srow + 64 * p, end - 1 - row) * (uint32_t)s.K + piece;
+    const uint8_t *w0 = we + (size_t)n0 * s.K;
+    const rsrc_t wb0 = buffer(w0), wb1 = buffer(GATED ? w0 + (size_t)s.N * s.K : w0);
+    const rsrc_t xb = buffer(a + (size_t)row * s.K);
+
+    const auto stage = [&](uint8_t *buf, int kb) {
+#pragma unroll
+        for (int p = 0; p < kTileN / 64; ++p)
+            load_to_lds(p < 2 ? wb0 : wb1, buf + p * 8192 + wid * 1024, woff[p], kb * 128);
+#pragma unroll
+        for (int p = 0; p < BM / 64; ++p) load_to_lds(xb, buf + kTileN * 128 + p * 8192 + wid * 1024, xoff[p], kb * 128);
+    };
+
+    // scales: one register per lane and group of 16 rows, one (or gate's and
+    // up's) per wave, loaded a block ahead
+    const rsrc_t asb = buffer(as + (size_t)row * KB), wsb = buffer(wse);
+    uint32_t asoff[MF], wsoff[HALF];
+#pragma unroll
+    for (int m = 0; m < MF; ++m)
+        asoff[m] = (uint32_t)min(wm * 16 * MF + 16 * m + r16, end - 1 - row) * (uint32_t)KB * 4;
+#pragma unroll
+    for (int h = 0; h < HALF; ++h)
+        wsoff[h] = (uint32_t)(min(n0 + h * s.N + wn * WCOLS, wrows - 1) / 128) * (uint32_t)KB * 4;
+
+    f32x4 acc[NF][MF] = {};
+    float sx[MF], sw[HALF];
+    const auto scales = [&](int kb) {
+#pragma unroll
+        for (int m = 0; m < MF; ++m) sx[m] = load_f32(asb, asoff[m], kb * 4);
+#pragma unroll
+        for (int h = 0; h < HALF; ++h) sw[h] = load_f32(wsb, wsoff[h], kb * 4);
+    };
+    const uint32_t plo = (uint32_t)((quad ^ (r16 & 7)) << 4), phi = plo ^ 64;
+    const uint32_t wlo = (uint32_t)(wn * WCOLS + r16) * 128 + plo, whi = (uint32_t)(wn * WCOLS + r16) * 128 + phi;
+    const uint32_t xrow = (uint32_t)(kTileN + wm * 16 * MF + r16) * 128;
+    const uint32_t xlo = xrow + plo, xhi = xrow + phi;
+    const auto multiply = [&](const uint8_t *buf, const float (&x)[MF], const float (&c)[HALF]) {
+        i32x8 xf[MF];
+#pragma unroll
+        for (int m = 0; m < MF; ++m) xf[m] = lds_operand(buf + xlo + 2048 * m, buf + xhi + 2048 * m);
+        const auto weights = [&](int n) {
+            const int at = GATED ? n / (NF / 2) * 128 * 128 + 2048 * (n % (NF / 2)) : 2048 * n;
+            return lds_operand(buf + wlo + at, buf + whi + at);
+        };
+        i32x8 wf = weights(0);
+#pragma unroll
+        for (int n = 0; n < NF; ++n) {
+            // the next weights are on their way while these are multiplied; the
+            // fence keeps the scheduler from fetching all of them at once
+            const i32x8 wnext = weights(n + 1 < NF ? n + 1 : n);
+            const int h = GATED ? n / (NF / 2) : 0;
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                const f32x4 d = mfma_128(wf, xf[m]);
+                const float sc = x[m] * c[h];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[n][m][i] = __builtin_fmaf(d[i], sc, acc[n][m][i]);
+                asm volatile("" : "+v"(acc[n][m]));   // added here, not sunk into the next block of K
+            }
+            wf = wnext;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    const auto step = [&](const uint8_t *cur, uint8_t *next, int kb) {
+        float x[MF], c[HALF];
+#pragma unroll
+        for (int m = 0; m < MF; ++m) x[m] = sx[m];
+#pragma unroll
+        for (int h = 0; h < HALF; ++h) c[h] = sw[h];
+        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the block has arrived
+        __syncthreads();                      // every wave's part; and the other buffer is free
+        if (kb + 1 < KB) {
+            stage(next, kb + 1);
+            scales(kb + 1);
+        }
+        multiply(cur, x, c);
+    };
+    stage(buf0, 0);
+    scales(0);
+    for (int kb = 0; kb < KB; kb += 2) {
+        step(buf0, buf1, kb);
+        if (kb + 1 < KB) step(buf1, buf0, kb + 1);
+    }
+
+    if constexpr (!GATED) {
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const int r = row + wm * 16 * MF + 16 * m + r16;
+#pragma unroll
+            for (int n = 0; n < NF; ++n) {
+                const int c = n0 + wn * WCOLS + 16 * n + 4 * quad;   // N % 8 == 0: all 4 in or all out
+                if (r >= end || c >= s.N) continue;
+                uint2 v;
+                v.x = pack_bf16x2(acc[n][m][0], acc[n][m][1]);
+                v.y = pack_bf16x2(acc[n][m][2], acc[n][m][3]);
+                *reinterpret_cast<uint2 *>(out + (size_t)r * s.N + c) = v;
+            }
+        }
+    } else {
+        // h takes the place of the gate's accumulators
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            float top = 0.0f;
+#pragma unroll
+            for (int n = 0; n < NF / 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    acc[n][m][i] = gate(acc[n][m][i], acc[n + NF / 2][m][i]);
+                    top = fmaxf(top, fabsf(acc[n][m][i]));
+                }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (quad == 0) amax[wn][wm * 16 * MF + 16 * m + r16] = top;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+            const int i = wm * 16 * MF + 16 * m + r16, r = row + i;
+            float top = 0.0f;
+#pragma unroll
+            for (int c = 0; c < WN; ++c) top = fmaxf(top, amax[c][i]);
+            const float scale = (top == 0.0f) ? 1.0f : top / 448.0f;
+            if (r >= end) continue;
+#pragma unroll
+            for (int n = 0; n < NF / 2; ++n) {
+                uint32_t q = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q |= f32_to_e4m3(acc[n][m][j] / scale) << (8 * j);
+                *reinterpret_cast<uint32_t *>(oq + (size_t)r * s.N + n0 + wn * WCOLS + 16 * n + 4 * quad) = q;
+            }
+            if (wn == 0 && quad == 0) oqs[(size_t)r * (s.N / 128) + ct] = scale;
+        }
+    }
+}
+
 constexpr int kStreamMT = 4, kStreamKS = 1;
 
 int64_t tile_slots(const ExpertShape &s, int BM) { return s.rows / BM + s.E; }
@@ -210,8 +419,23 @@ bool expert_grid_fits(const ExpertShape &s, bool gated) {
     return cols <= 65535 && tile_slots(s, 16) * 1024 < (int64_t(1) << 32);
 }
 
+namespace {
+
+template <int BM, int WN, bool GATED>
+hipError_t launch_tile(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
+                       const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
+    const int slots = (int)tile_slots(s, BM), cols = GATED ? s.N / 128 : (s.N + kTileN - 1) / kTileN;
+    const int64_t blocks = (int64_t)((slots + 7) / 8) * 8 * cols;
+    hipLaunchKernelGGL((ep_expert_tile_kernel<BM, WN, GATED>), dim3((unsigned)blocks), dim3(kTileThreads), 0, stream,
+                       s, offset, a, as, w, ws, out, q, qs, slots, cols);
+    return hipGetLastError();
+}
+
+}  // namespace
+
 hipError_t launch_expert_gemm(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                               const uint8_t *w, const float *ws, uint16_t *out, hipStream_t stream) {
+    if (s.rows / s.E >= 64) return launch_tile<256, 2, false>(s, offset, a, as, w, ws, out, nullptr, nullptr, stream);
     const dim3 grid((unsigned)tile_slots(s, 16 * kStreamMT), (unsigned)((s.N + 255) / 256));
     hipLaunchKernelGGL((ep_expert_stream_kernel<kStreamMT, kStreamKS, false>), grid,
                        dim3(kWave * kColWaves * kStreamKS), 0, stream, s, offset, a, as, w, ws, out, nullptr, nullptr);
@@ -220,6 +444,7 @@ hipError_t launch_expert_gemm(const ExpertShape &s, const int32_t *offset, const
 
 hipError_t launch_expert_gated(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                                const uint8_t *w, const float *ws, uint8_t *q, float *qs, hipStream_t stream) {
+    if (s.rows / s.E >= 64) return launch_tile<256, 2, true>(s, offset, a, as, w, ws, nullptr, q, qs, stream);
     const dim3 grid((unsigned)tile_slots(s, 16 * kStreamMT), (unsigned)(s.N / 128));
     hipLaunchKernelGGL((ep_expert_stream_kernel<kStreamMT, kStreamKS, true>), grid,
                        dim3(kWave * kColWaves * kStreamKS), 0, stream, s, offset, a, as, w, ws, nullptr, q, qs);
