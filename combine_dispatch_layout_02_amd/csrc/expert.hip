@@ -246,7 +246,11 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     __shared__ int found;
     __shared__ float amax[GATED ? WN : 1][GATED ? BM : 1];
 
-    const int per = 8 * cols, sb = blockIdx.x / per, in = blockIdx.x % per;
+    // consecutive blocks go to the 8 XCDs in turn; each XCD takes a contiguous
+    // eighth of the tiles, 8 row tiles by all columns at a time, so that the
+    // 32 blocks it runs together share their operands in its L2
+    const int tile = (int)blockIdx.x;
+    const int per = 8 * cols, sb = tile / per, in = tile % per;
     const int slot = sb * 8 + in % 8, ct = in / 8;
     if (slot >= slots) return;
     int e, row, end;
@@ -278,12 +282,12 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     const rsrc_t wb0 = buffer(w0), wb1 = buffer(GATED ? w0 + (size_t)s.N * s.K : w0);
     const rsrc_t xb = buffer(a + (size_t)row * s.K);
 
-    const auto stage = [&](uint8_t *buf, int kb) {
-#pragma unroll
-        for (int p = 0; p < kTileN / 64; ++p)
+    constexpr int PIECES = (kTileN + BM) / 64;
+    const auto stage = [&](uint8_t *buf, int kb, int p) {   // piece p of a block of K
+        if (p < kTileN / 64)
             load_to_lds(p < 2 ? wb0 : wb1, buf + p * 8192 + wid * 1024, woff[p], kb * 128);
-#pragma unroll
-        for (int p = 0; p < BM / 64; ++p) load_to_lds(xb, buf + kTileN * 128 + p * 8192 + wid * 1024, xoff[p], kb * 128);
+        else
+            load_to_lds(xb, buf + p * 8192 + wid * 1024, xoff[p - kTileN / 64], kb * 128);
     };
 
     // scales: one register per lane and group of 16 rows, one (or gate's and
@@ -309,7 +313,7 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     const uint32_t wlo = (uint32_t)(wn * WCOLS + r16) * 128 + plo, whi = (uint32_t)(wn * WCOLS + r16) * 128 + phi;
     const uint32_t xrow = (uint32_t)(kTileN + wm * 16 * MF + r16) * 128;
     const uint32_t xlo = xrow + plo, xhi = xrow + phi;
-    const auto multiply = [&](const uint8_t *buf, const float (&x)[MF], const float (&c)[HALF]) {
+    const auto multiply = [&](const uint8_t *buf, const float (&x)[MF], const float (&c)[HALF], const auto &between) {
         i32x8 xf[MF];
 #pragma unroll
         for (int m = 0; m < MF; ++m) xf[m] = lds_operand(buf + xlo + 2048 * m, buf + xhi + 2048 * m);
@@ -317,25 +321,45 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
             const int at = GATED ? n / (NF / 2) * 128 * 128 + 2048 * (n % (NF / 2)) : 2048 * n;
             return lds_operand(buf + wlo + at, buf + whi + at);
         };
-        i32x8 wf = weights(0);
-#pragma unroll
-        for (int n = 0; n < NF; ++n) {
-            // the next weights are on their way while these are multiplied; the
-            // fence keeps the scheduler from fetching all of them at once
-            const i32x8 wnext = weights(n + 1 < NF ? n + 1 : n);
-            const int h = GATED ? n / (NF / 2) : 0;
+        const auto add = [&](int n, const f32x4 (&d)[MF]) {
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
-                const f32x4 d = mfma_128(wf, xf[m]);
-                const float sc = x[m] * c[h];
+                const float sc = x[m] * c[GATED ? n / (NF / 2) : 0];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][m][i] = __builtin_fmaf(d[i], sc, acc[n][m][i]);
+                for (int i = 0; i < 4; ++i) acc[n][m][i] = __builtin_fmaf(d[m][i], sc, acc[n][m][i]);
                 asm volatile("" : "+v"(acc[n][m]));   // added here, not sunk into the next block of K
             }
-            wf = wnext;
+        };
+        i32x8 wf = weights(0);
+        f32x4 last[MF];
+#pragma unroll
+        for (int n = 0; n < NF; ++n) {
+            // the next weights are on their way and the last products are being
+            // scaled while these are multiplied; the fence keeps the scheduler
+            // from fetching all of them at once
+            const i32x8 wnext = weights(n + 1 < NF ? n + 1 : n);
+            f32x4 d[MF];
+#pragma unroll
+            for (int m = 0; m < MF; ++m) d[m] = mfma_128(wf, xf[m]);
+            if (n > 0) add(n - 1, last);
+            between(n);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // 2 reads of LDS, then in turn
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // and 4 vector ones
+            }
             __builtin_amdgcn_sched_barrier(0);
+            wf = wnext;
+#pragma unroll
+            for (int m = 0; m < MF; ++m) last[m] = d[m];
         }
+        add(NF - 1, last);
     };
+    // The next block's loads are issued a few at a time between the matrix
+    // instructions: all at once they fill the memory pipe's queue and every
+    // wave waits at the start of the block.  The last block loads itself again
+    // (a branch here would cost registers).
     const auto step = [&](const uint8_t *cur, uint8_t *next, int kb) {
         float x[MF], c[HALF];
 #pragma unroll
@@ -344,18 +368,21 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
         for (int h = 0; h < HALF; ++h) c[h] = sw[h];
         __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the block has arrived
         __syncthreads();                      // every wave's part; and the other buffer is free
-        if (kb + 1 < KB) {
-            stage(next, kb + 1);
-            scales(kb + 1);
-        }
-        multiply(cur, x, c);
+        const int after = min(kb + 1, KB - 1);
+        scales(after);
+        multiply(cur, x, c, [&](int n) {
+#pragma unroll
+            for (int p = n * PIECES / NF; p < (n + 1) * PIECES / NF; ++p) stage(next, after, p);
+        });
     };
-    stage(buf0, 0);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) stage(buf0, 0, p);
     scales(0);
     for (int kb = 0; kb < KB; kb += 2) {
         step(buf0, buf1, kb);
         if (kb + 1 < KB) step(buf1, buf0, kb + 1);
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);
 
     if constexpr (!GATED) {
 #pragma unroll
