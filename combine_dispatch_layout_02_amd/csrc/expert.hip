@@ -28,6 +28,64 @@ __device__ __forceinline__ f32x4 mfma_128(i32x8 a, i32x8 b) {
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
 }
 
+// The 8-bit matrix instruction adds 8 products at a time and drops what lies
+// below 2^-13 of their largest (measured): over random blocks of 128 the sum is
+// off by 1.5e-5 of itself.  That vanishes in a bf16 result (half a step is
+// 2^-9 to 2^-8), so ep_expert_gemm takes it.  The gated product hands on its
+// groups' scales in binary32; it widens its operands to f16, exactly, and takes
+// the 16-bit instruction (8e-9 on the same blocks, measured) at half the rate.
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+struct Wide {
+    f16x8 v[4];
+};
+
+__device__ __forceinline__ Wide widen(i32x8 b) {
+    Wide w;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b[i], 1.0f, false);
+        const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b[i], 1.0f, true);
+        w.v[i / 2][4 * (i % 2) + 0] = lo[0];
+        w.v[i / 2][4 * (i % 2) + 1] = lo[1];
+        w.v[i / 2][4 * (i % 2) + 2] = hi[0];
+        w.v[i / 2][4 * (i % 2) + 3] = hi[1];
+    }
+    return w;
+}
+
+__device__ __forceinline__ f32x4 mfma_32(f16x8 a, f16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// The operand of a kernel, and MT products of one with MT others, side by side
+// so that no instruction waits for the one before it.
+template <bool WIDE>
+struct Operand;
+template <>
+struct Operand<false> {
+    typedef i32x8 type;
+    static __device__ __forceinline__ type make(i32x8 b) { return b; }
+    template <int MT>
+    static __device__ __forceinline__ void multiply(const type &a, const type (&b)[MT], f32x4 (&d)[MT]) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) d[m] = mfma_128(a, b[m]);
+    }
+};
+template <>
+struct Operand<true> {
+    typedef Wide type;
+    static __device__ __forceinline__ type make(i32x8 b) { return widen(b); }
+    template <int MT>
+    static __device__ __forceinline__ void multiply(const type &a, const type (&b)[MT], f32x4 (&d)[MT]) {
+        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) d[m] = mfma_32(a.v[k], b[m].v[k], k ? d[m] : zero);
+    }
+};
+
 // A lane's 32 bytes of a 128-byte block: 16 at 16 (l / 16), 16 more 64 on, so
 // that one load instruction covers whole 64-byte pieces of 16 rows.
 __device__ __forceinline__ i32x8 ld_operand(const uint8_t *p) {
@@ -93,6 +151,7 @@ __global__ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
     __shared__ int found;
     __shared__ f32x4 part[KS > 1 ? KS - 1 : 1][KS > 1 ? kColWaves : 1][KS > 1 ? 2 * MT : 1][kWave];
     __shared__ float amax[GATED ? kColWaves : 1][GATED ? 16 * MT : 1];
+    typedef Operand<GATED> Op;
     int e, row, end;
     if (!find_tile(off, s, blockIdx.x, 16 * MT, &found, &e, &row, &end)) return;
 
@@ -122,18 +181,25 @@ __global__ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
     f32x4 acc[2][MT] = {};
     const int kb0 = KB * ks / KS, kb1 = KB * (ks + 1) / KS;
     for (int kb = kb0; kb < kb1; ++kb) {
-        const i32x8 f0 = ld_operand(w0 + (size_t)kb * 128), f1 = ld_operand(w1 + (size_t)kb * 128);
+        const auto f0 = Op::make(ld_operand(w0 + (size_t)kb * 128)), f1 = Op::make(ld_operand(w1 + (size_t)kb * 128));
         const float c0 = ws0[kb], c1 = ws1[kb];
+        typename Op::type x[MT];
+        float sc[MT];
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            const i32x8 x = ld_operand(ap[m] + (size_t)kb * 128);
-            const float sc = asp[m][kb];
-            const f32x4 d0 = mfma_128(f0, x), d1 = mfma_128(f1, x);
-            const float s0 = sc * c0, s1 = sc * c1;
+            x[m] = Op::make(ld_operand(ap[m] + (size_t)kb * 128));
+            sc[m] = asp[m][kb];
+        }
+        f32x4 d0[MT], d1[MT];
+        Op::multiply(f0, x, d0);
+        Op::multiply(f1, x, d1);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            const float s0 = sc[m] * c0, s1 = sc[m] * c1;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                acc[0][m][i] = __builtin_fmaf(d0[i], s0, acc[0][m][i]);
-                acc[1][m][i] = __builtin_fmaf(d1[i], s1, acc[1][m][i]);
+                acc[0][m][i] = __builtin_fmaf(d0[m][i], s0, acc[0][m][i]);
+                acc[1][m][i] = __builtin_fmaf(d1[m][i], s1, acc[1][m][i]);
             }
         }
     }
@@ -241,6 +307,7 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     constexpr int WM = 8 / WN, NF = kTileN / WN / 16, MF = BM / WM / 16;
     constexpr int HALF = GATED ? 2 : 1;            // gate and up, or one product
     constexpr int WCOLS = kTileN / HALF / WN;      // columns of the result per wave
+    typedef Operand<GATED> Op;
     __shared__ __attribute__((aligned(16))) uint8_t buf0[(kTileN + BM) * 128];
     __shared__ __attribute__((aligned(16))) uint8_t buf1[(kTileN + BM) * 128];
     __shared__ int found;
@@ -268,13 +335,12 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     // staging: pass p of the block covers 64 rows, a wave 8 of them
     const int srow = wid * 8 + (lane >> 3);                    // + 64 p
     const uint32_t piece = (uint32_t)(((lane & 7) ^ (srow & 7)) << 4);
-    uint32_t woff[kTileN / 64], xoff[BM / 64];
+    // gated: all 128 rows of gate and of up are there, 64 rows on is a scalar
+    // offset; else the last tile's rows past the end repeat the last one
+    uint32_t woff[GATED ? 1 : kTileN / 64], xoff[BM / 64];
 #pragma unroll
-    for (int p = 0; p < kTileN / 64; ++p) {
-        const int r = srow + 64 * p;
-        const int n = GATED ? r % 128 : min(r, wrows - 1 - n0);
-        woff[p] = (uint32_t)n * (uint32_t)s.K + piece;
-    }
+    for (int p = 0; p < (GATED ? 1 : kTileN / 64); ++p)
+        woff[p] = (uint32_t)(GATED ? srow : min(srow + 64 * p, wrows - 1 - n0)) * (uint32_t)s.K + piece;
 #pragma unroll
     for (int p = 0; p < BM / 64; ++p)
         xoff[p] = (uint32_t)min(srow + 64 * p, end - 1 - row) * (uint32_t)s.K + piece;
@@ -284,8 +350,10 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
 
     constexpr int PIECES = (kTileN + BM) / 64;
     const auto stage = [&](uint8_t *buf, int kb, int p) {   // piece p of a block of K
-        if (p < kTileN / 64)
-            load_to_lds(p < 2 ? wb0 : wb1, buf + p * 8192 + wid * 1024, woff[p], kb * 128);
+        if (GATED && p < kTileN / 64)
+            load_to_lds(p < 2 ? wb0 : wb1, buf + p * 8192 + wid * 1024, woff[0], (p & 1) * 64 * s.K + kb * 128);
+        else if (p < kTileN / 64)
+            load_to_lds(wb0, buf + p * 8192 + wid * 1024, woff[p], kb * 128);
         else
             load_to_lds(xb, buf + p * 8192 + wid * 1024, xoff[p - kTileN / 64], kb * 128);
     };
@@ -314,9 +382,9 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     const uint32_t xrow = (uint32_t)(kTileN + wm * 16 * MF + r16) * 128;
     const uint32_t xlo = xrow + plo, xhi = xrow + phi;
     const auto multiply = [&](const uint8_t *buf, const float (&x)[MF], const float (&c)[HALF], const auto &between) {
-        i32x8 xf[MF];
+        typename Op::type xf[MF];
 #pragma unroll
-        for (int m = 0; m < MF; ++m) xf[m] = lds_operand(buf + xlo + 2048 * m, buf + xhi + 2048 * m);
+        for (int m = 0; m < MF; ++m) xf[m] = Op::make(lds_operand(buf + xlo + 2048 * m, buf + xhi + 2048 * m));
         const auto weights = [&](int n) {
             const int at = GATED ? n / (NF / 2) * 128 * 128 + 2048 * (n % (NF / 2)) : 2048 * n;
             return lds_operand(buf + wlo + at, buf + whi + at);
@@ -339,22 +407,25 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
             // from fetching all of them at once
             const i32x8 wnext = weights(n + 1 < NF ? n + 1 : n);
             f32x4 d[MF];
-#pragma unroll
-            for (int m = 0; m < MF; ++m) d[m] = mfma_128(wf, xf[m]);
-            if (n > 0) add(n - 1, last);
+            Op::multiply(Op::make(wf), xf, d);
             between(n);
-            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // 2 reads of LDS, then in turn
+            if constexpr (GATED) {   // no registers to spare for a second set of products
+                add(n, d);
+            } else {
+                if (n > 0) add(n - 1, last);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // 2 reads of LDS, then in turn
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
-                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // and 4 vector ones
+                for (int m = 0; m < MF; ++m) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // and 4 vector ones
+                }
+#pragma unroll
+                for (int m = 0; m < MF; ++m) last[m] = d[m];
             }
             __builtin_amdgcn_sched_barrier(0);
             wf = wnext;
-#pragma unroll
-            for (int m = 0; m < MF; ++m) last[m] = d[m];
         }
-        add(NF - 1, last);
+        if constexpr (!GATED) add(NF - 1, last);
     };
     // The next block's loads are issued a few at a time between the matrix
     // instructions: all at once they fill the memory pipe's queue and every
