@@ -86,10 +86,46 @@ struct Operand<true> {
     }
 };
 
-// A lane's 32 bytes of a 128-byte block: 16 at 16 (l / 16), 16 more 64 on, so
-// that one load instruction covers whole 64-byte pieces of 16 rows.
-__device__ __forceinline__ i32x8 ld_operand(const uint8_t *p) {
-    const vec16 lo = ld16(p), hi = ld16(p + 64);
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+// A barrier that waits for the waves alone: __syncthreads also waits for every
+// load on its way to LDS.  What a wave needs of those it waits for itself.
+__device__ __forceinline__ void barrier_only() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A buffer of `bytes` bytes (2^31 - 1 at most) from a wave-uniform base: a load
+// is then one 32-bit register of offset per lane and a scalar one per block of
+// K, and reads 0 past the end.
+__device__ __forceinline__ rsrc_t buffer(const void *p, int64_t bytes = 0x7FFFFFFF) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0,
+                                             (int)(bytes < 0x7FFFFFFF ? bytes : 0x7FFFFFFF), 0x00020000);
+}
+
+// 16 bytes per lane from memory into LDS at base + 16 lane, without a register.
+__device__ __forceinline__ void load_to_lds(rsrc_t b, uint8_t *lds, uint32_t off, uint32_t soff) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void *)lds, 16, (int)off, (int)soff,
+                                             0, 0);
+}
+
+__device__ __forceinline__ float load_f32(rsrc_t b, uint32_t off, uint32_t soff) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, (int)soff, 0));
+}
+
+__device__ __forceinline__ f32x4 load_4f32(rsrc_t b, uint32_t off, uint32_t soff) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, (int)off, (int)soff, 0));
+}
+
+// A lane's 32 bytes of a row of a tile in LDS, given where its two pieces lie.
+// Rows are 128 bytes, and their 16-byte pieces are permuted by the row (piece c
+// lies at c ^ (r % 8)), so that the 8 lanes of one LDS cycle touch every bank
+// once; rows 16 apart have the same permutation.
+__device__ __forceinline__ i32x8 lds_operand(const uint8_t *lo16, const uint8_t *hi16) {
+    const vec16 lo = ld16(lo16), hi = ld16(hi16);
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
@@ -138,81 +174,183 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape 
 // h = g / (1 + e^-g) u
 __device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + expf(-g)) * u; }
 
+// ---------------------------------------------------------------- few rows
+
 constexpr int kColWaves = 8;   // waves side by side: 16 weight rows twice each
 
 // BM = 16 MT rows by 256 weight rows (gated: 128 columns of gate and the same
-// 128 of up, one scale group of the result), K split over KS waves whose
-// parts are added in LDS in wave order.  Operands go straight from memory to
-// registers.
+// 128 of up, one scale group of the result), K split over KS groups of 8 waves
+// whose parts are added in LDS in their order.  Here the weights are what
+// counts: each is read once.  Loading them straight into the operands' layout
+// costs the address unit a cycle per lane pair, as neighbouring lanes hold
+// different rows, and bounds the kernel at a third of the memory rate; so each
+// wave copies its 32 weight rows' next block of K (4 KiB, whole 128-byte
+// lines) into its own part of LDS and reads the operands from there, with two
+// blocks in flight and no barrier.  The rows of a are shared by the waves: XB
+// blocks of K at a time, two buffers, a barrier per change.
 template <int MT, int KS, bool GATED>
-__global__ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
+__global__ __launch_bounds__(64 * kColWaves * KS, MT == 4 ? 2 : 4) void ep_expert_stream_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
-    uint16_t *out, uint8_t *oq, float *oqs) {
+    uint16_t *out, uint8_t *oq, float *oqs, int cols) {
+    constexpr int XB = MT == 4 ? 1 : 2;              // blocks of K of a's rows per change
+    constexpr int XBYTES = 16 * MT * 128 * XB;       // 4 or 8 KiB: a piece of XBYTES / 8 per wave
+    __shared__ __attribute__((aligned(16))) uint8_t wbuf0[kColWaves * KS * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t wbuf1[kColWaves * KS * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t xbuf0[KS * XBYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t xbuf1[KS * XBYTES];
     __shared__ int found;
-    __shared__ f32x4 part[KS > 1 ? KS - 1 : 1][KS > 1 ? kColWaves : 1][KS > 1 ? 2 * MT : 1][kWave];
     __shared__ float amax[GATED ? kColWaves : 1][GATED ? 16 * MT : 1];
     typedef Operand<GATED> Op;
     int e, row, end;
-    if (!find_tile(off, s, blockIdx.x, 16 * MT, &found, &e, &row, &end)) return;
+    // columns first: an expert's blocks spread over the XCDs, also where only a
+    // few experts have rows
+    const int ct = blockIdx.x % cols;
+    if (!find_tile(off, s, blockIdx.x / cols, 16 * MT, &found, &e, &row, &end)) return;
 
-    const int lane = threadIdx.x & (kWave - 1), wid = threadIdx.x / kWave;
+    const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int col = wid % kColWaves, ks = wid / kColWaves;
     const int r16 = lane & 15, quad = lane >> 4;
     const int KB = s.K / 128;
     const int wrows = GATED ? 2 * s.N : s.N;
     // the two groups of 16 weight rows of this wave
-    const int n0 = GATED ? (int)blockIdx.y * 128 + col * 16 : (int)blockIdx.y * 256 + col * 32;
+    const int n0 = GATED ? ct * 128 + col * 16 : ct * 256 + col * 32;
     const int n1 = GATED ? n0 + s.N : n0 + 16;
     const uint8_t *we = w + (size_t)e * wrows * s.K;
     const float *wse = ws + (size_t)e * ((wrows + 127) / 128) * KB;
-    const uint8_t *w0 = we + (size_t)min(n0 + r16, wrows - 1) * s.K + quad * 16;
-    const uint8_t *w1 = we + (size_t)min(n1 + r16, wrows - 1) * s.K + quad * 16;
-    const float *ws0 = wse + (size_t)(min(n0, wrows - 1) / 128) * KB;
-    const float *ws1 = wse + (size_t)(min(n1, wrows - 1) / 128) * KB;
-    const uint8_t *ap[MT];
-    const float *asp[MT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const int r = min(row + 16 * m + r16, end - 1);   // rows past the segment repeat its last one
-        ap[m] = a + (size_t)r * s.K + quad * 16;
-        asp[m] = as + (size_t)r * KB;
-    }
+    // this wave's blocks of K; every group walks `steps` of them (barriers)
+    const int first = KB * ks / KS, n = KB * (ks + 1) / KS - first, steps = (KB + KS - 1) / KS;
 
+    // staging: instruction i of a wave covers 8 rows, 8 lanes each
+    const int srow = lane >> 3;
+    const uint32_t piece = (uint32_t)(((lane & 7) ^ srow) << 4);
+    const int m0 = min(n0, wrows - 1), m1 = min(n1, wrows - 1);   // rows past the end repeat the last one
+    const rsrc_t wb0 = buffer(we + (size_t)m0 * s.K), wb1 = buffer(we + (size_t)m1 * s.K);
+    uint32_t woff[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        woff[i] = (uint32_t)min(srow + 8 * (i & 1), wrows - 1 - (i < 2 ? m0 : m1)) * (uint32_t)s.K + piece;
+    // a block past the last is read from past the buffer's end: zeros, no memory
+    // traffic, and the same count of loads under way in every step
+    const auto past = [&](int i) { return i < n ? 0u : 0x80000000u; };
+    const auto stage_w = [&](uint8_t *buf, int i) {
+        const uint32_t k = (uint32_t)(first + i) * 128;
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+            load_to_lds(p < 2 ? wb0 : wb1, buf + wid * 4096 + p * 1024, woff[p] | past(i), k);
+    };
+    // a's rows: [block of K][row][128 bytes], 8 lines per wave (where there are
+    // fewer pieces than waves, two waves bring the same one)
+    const rsrc_t xb = buffer(a + (size_t)row * s.K);
+    constexpr int PIECES = XBYTES / 1024;
+    const int xline = col % PIECES * 8 + srow, xr = xline % (16 * MT), xblock = xline / (16 * MT);
+    const uint32_t xoff = (uint32_t)min(xr, end - 1 - row) * (uint32_t)s.K + (uint32_t)xblock * 128 +
+                          (uint32_t)(((lane & 7) ^ (xr & 7)) << 4);
+    const auto stage_x = [&](uint8_t *buf, int i) {   // blocks i .. i + XB - 1 of K
+        load_to_lds(xb, buf + ks * XBYTES + col % PIECES * 1024, xoff | past(i + xblock), (uint32_t)(first + i) * 128);
+    };
+    // scales, four blocks of K at a time
+    const rsrc_t asb = buffer(as + (size_t)row * KB, (s.rows - row) * KB * 4);
+    const rsrc_t wsb = buffer(wse, (int64_t)((wrows + 127) / 128) * KB * 4);
+    uint32_t asoff[MT], wsoff[2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) asoff[m] = (uint32_t)min(16 * m + r16, end - 1 - row) * (uint32_t)KB * 4;
+    wsoff[0] = (uint32_t)(m0 / 128) * (uint32_t)KB * 4;
+    wsoff[1] = (uint32_t)(m1 / 128) * (uint32_t)KB * 4;
+
+    const uint32_t plo = (uint32_t)(r16 * 128 + ((quad ^ (r16 & 7)) << 4)), phi = plo ^ 64;
     f32x4 acc[2][MT] = {};
-    const int kb0 = KB * ks / KS, kb1 = KB * (ks + 1) / KS;
-    for (int kb = kb0; kb < kb1; ++kb) {
-        const auto f0 = Op::make(ld_operand(w0 + (size_t)kb * 128)), f1 = Op::make(ld_operand(w1 + (size_t)kb * 128));
-        const float c0 = ws0[kb], c1 = ws1[kb];
-        typename Op::type x[MT];
-        float sc[MT];
+    f32x4 cx[MT], cw[2], nx[MT], nw[2];
+    const auto scales = [&](int i) {
+        const uint32_t k = (uint32_t)(first + i) * 4;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            x[m] = Op::make(ld_operand(ap[m] + (size_t)kb * 128));
-            sc[m] = asp[m][kb];
+        for (int m = 0; m < MT; ++m) nx[m] = load_4f32(asb, asoff[m] | past(i), k);
+        nw[0] = load_4f32(wsb, wsoff[0] | past(i), k);
+        nw[1] = load_4f32(wsb, wsoff[1] | past(i), k);
+    };
+    const auto step = [&](uint8_t *wbuf, const uint8_t *xbuf, int i, int part, int j) {
+        // this block of weights has arrived: the wait before the change of a's
+        // rows covers it, or 5 later loads to LDS may be under way, the next
+        // block's and one piece of a's rows (other loads only add to those)
+        if (part > 0) {
+            __builtin_amdgcn_s_waitcnt(0x0F75);   // vmcnt(5)
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
         }
-        f32x4 d0[MT], d1[MT];
-        Op::multiply(f0, x, d0);
-        Op::multiply(f1, x, d1);
+        const uint8_t *wp = wbuf + wid * 4096;
+        const i32x8 f0 = lds_operand(wp + plo, wp + phi), f1 = lds_operand(wp + 2048 + plo, wp + 2048 + phi);
+        const uint8_t *xp = xbuf + ks * XBYTES + part * (16 * MT * 128);
+        i32x8 xr[MT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            const float s0 = sc[m] * c0, s1 = sc[m] * c1;
+        for (int m = 0; m < MT; ++m) xr[m] = lds_operand(xp + 2048 * m + plo, xp + 2048 * m + phi);
+        // the operands are in registers: their place takes the block after next
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        __builtin_amdgcn_sched_barrier(0);
+        stage_w(wbuf, i + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        typename Op::type x[MT];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                acc[0][m][i] = __builtin_fmaf(d0[m][i], s0, acc[0][m][i]);
-                acc[1][m][i] = __builtin_fmaf(d1[m][i], s1, acc[1][m][i]);
+        for (int m = 0; m < MT; ++m) x[m] = Op::make(xr[m]);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            f32x4 d[MT];
+            Op::multiply(Op::make(f ? f1 : f0), x, d);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const float sc = cx[m][j] * cw[f][j];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[f][m][q] = __builtin_fmaf(d[m][q], sc, acc[f][m][q]);
+                asm volatile("" : "+v"(acc[f][m]));   // added here, not after the next loads
             }
         }
-    }
+    };
+    const auto group = [&](int i, bool whole) {   // four blocks of K
+#pragma unroll
+        for (int m = 0; m < MT; ++m) cx[m] = nx[m];
+        cw[0] = nw[0];
+        cw[1] = nw[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (!whole && i + j >= steps) break;
+            if (j % XB == 0) {
+                // a's rows for this change have arrived in every wave (behind
+                // them only the next block of weights may be under way: 4
+                // loads); the other buffer is free
+                __builtin_amdgcn_s_waitcnt(0x0F74);   // vmcnt(4)
+                barrier_only();
+                stage_x((j / XB) % 2 ? xbuf0 : xbuf1, i + j + XB);
+            }
+            if (whole || i + j < n)   // wave-uniform
+                step(j % 2 ? wbuf1 : wbuf0, (j / XB) % 2 ? xbuf1 : xbuf0, i + j, j % XB, j);
+            else
+                __builtin_amdgcn_s_waitcnt(0x0F70);
+            if (j == 0) scales(i + 4);
+        }
+    };
+    stage_w(wbuf0, 0);
+    stage_x(xbuf0, 0);
+    scales(0);
+    stage_w(wbuf1, 1);
+    int i = 0;
+    for (; i + 4 <= KB / KS; i += 4) group(i, true);
+    if (i < steps) group(i, false);
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+
     if constexpr (KS > 1) {
+        // the parts of K, in the place of the weights
+        static_assert((KS - 1) * 2 * MT * 1024 <= KS * 4096, "they fit");
+        __syncthreads();
+        f32x4 *part = reinterpret_cast<f32x4 *>(wbuf0);
         if (ks > 0)
 #pragma unroll
-            for (int m = 0; m < 2 * MT; ++m) part[ks - 1][col][m][lane] = acc[m & 1][m >> 1];
+            for (int m = 0; m < 2 * MT; ++m)
+                part[(((ks - 1) * kColWaves + col) * 2 * MT + m) * kWave + lane] = acc[m & 1][m >> 1];
         __syncthreads();
         if (ks == 0)
 #pragma unroll
             for (int p = 0; p < KS - 1; ++p)
 #pragma unroll
-                for (int m = 0; m < 2 * MT; ++m) acc[m & 1][m >> 1] += part[p][col][m][lane];
+                for (int m = 0; m < 2 * MT; ++m)
+                    acc[m & 1][m >> 1] += part[((p * kColWaves + col) * 2 * MT + m) * kWave + lane];
     }
 
     if constexpr (!GATED) {
@@ -260,7 +398,7 @@ __global__ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
             for (int i = 0; i < 4; ++i) q |= f32_to_e4m3(h[m][i] / scale) << (8 * i);
             if (r >= end) continue;
             *reinterpret_cast<uint32_t *>(oq + (size_t)r * s.N + n0 + 4 * quad) = q;
-            if (col == 0 && quad == 0) oqs[(size_t)r * (s.N / 128) + blockIdx.y] = scale;
+            if (col == 0 && quad == 0) oqs[(size_t)r * (s.N / 128) + ct] = scale;
         }
     }
 }
@@ -268,33 +406,6 @@ __global__ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
 // ---------------------------------------------------------------- many rows
 
 constexpr int kTileThreads = 512, kTileN = 256;   // 8 waves; weight rows of a tile
-
-typedef __amdgpu_buffer_rsrc_t rsrc_t;
-
-// Buffers of at most 2^31 bytes from a wave-uniform base: a load is then one
-// 32-bit register of offset per lane and a scalar one per block of K.
-__device__ __forceinline__ rsrc_t buffer(const void *p) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, 0x7FFFFFFF, 0x00020000);
-}
-
-// 16 bytes per lane from memory into LDS at base + 16 lane, without a register.
-__device__ __forceinline__ void load_to_lds(rsrc_t b, uint8_t *lds, uint32_t off, uint32_t soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (__attribute__((address_space(3))) void *)lds, 16, (int)off, (int)soff,
-                                             0, 0);
-}
-
-__device__ __forceinline__ float load_f32(rsrc_t b, uint32_t off, uint32_t soff) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(b, (int)off, (int)soff, 0));
-}
-
-// A lane's 32 bytes of a row of a tile in LDS, given where its two pieces lie.
-// Rows are 128 bytes, and their 16-byte pieces are permuted by the row (piece c
-// lies at c ^ (r % 8)), so that the 8 lanes of one LDS cycle touch every bank
-// once; rows 16 apart have the same permutation.
-__device__ __forceinline__ i32x8 lds_operand(const uint8_t *lo16, const uint8_t *hi16) {
-    const vec16 lo = ld16(lo16), hi = ld16(hi16);
-    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
 
 // One block: BM rows by 256 weight rows (gated: 128 gate rows and the matching
 // 128 up rows), 8 waves, WN of them side by side.  Both operands of a block of
@@ -506,15 +617,13 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     }
 }
 
-constexpr int kStreamMT = 4, kStreamKS = 1;
-
 int64_t tile_slots(const ExpertShape &s, int BM) { return s.rows / BM + s.E; }
 
 }  // namespace
 
 bool expert_grid_fits(const ExpertShape &s, bool gated) {
     const int64_t cols = gated ? s.N / 128 : (s.N + 255) / 256;
-    return cols <= 65535 && tile_slots(s, 16) * 1024 < (int64_t(1) << 32);
+    return tile_slots(s, 16) * cols * 1024 < (int64_t(1) << 32);
 }
 
 namespace {
@@ -529,24 +638,37 @@ hipError_t launch_tile(const ExpertShape &s, const int32_t *offset, const uint8_
     return hipGetLastError();
 }
 
+template <int MT, int KS, bool GATED>
+hipError_t launch_stream(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
+                         const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
+    const int cols = GATED ? s.N / 128 : (s.N + 255) / 256;
+    hipLaunchKernelGGL((ep_expert_stream_kernel<MT, KS, GATED>), dim3((unsigned)(tile_slots(s, 16 * MT) * cols)),
+                       dim3(kWave * kColWaves * KS), 0, stream, s, offset, a, as, w, ws, out, q, qs, cols);
+    return hipGetLastError();
+}
+
+template <bool GATED>
+hipError_t launch_product(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
+                          const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
+    const int64_t mean = s.rows / s.E;   // rows of an expert, as far as the host knows them
+    if (mean >= 64) return launch_tile<256, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+    if (mean >= 24) return launch_stream<4, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+    if (mean >= 10) return launch_stream<2, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+    const int64_t blocks = (s.rows < s.E ? s.rows : s.E) * (GATED ? s.N / 128 : (s.N + 255) / 256);
+    if (blocks >= 512) return launch_stream<1, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+    return launch_stream<1, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+}
+
 }  // namespace
 
 hipError_t launch_expert_gemm(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                               const uint8_t *w, const float *ws, uint16_t *out, hipStream_t stream) {
-    if (s.rows / s.E >= 64) return launch_tile<256, 2, false>(s, offset, a, as, w, ws, out, nullptr, nullptr, stream);
-    const dim3 grid((unsigned)tile_slots(s, 16 * kStreamMT), (unsigned)((s.N + 255) / 256));
-    hipLaunchKernelGGL((ep_expert_stream_kernel<kStreamMT, kStreamKS, false>), grid,
-                       dim3(kWave * kColWaves * kStreamKS), 0, stream, s, offset, a, as, w, ws, out, nullptr, nullptr);
-    return hipGetLastError();
+    return launch_product<false>(s, offset, a, as, w, ws, out, nullptr, nullptr, stream);
 }
 
 hipError_t launch_expert_gated(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                                const uint8_t *w, const float *ws, uint8_t *q, float *qs, hipStream_t stream) {
-    if (s.rows / s.E >= 64) return launch_tile<256, 2, true>(s, offset, a, as, w, ws, nullptr, q, qs, stream);
-    const dim3 grid((unsigned)tile_slots(s, 16 * kStreamMT), (unsigned)(s.N / 128));
-    hipLaunchKernelGGL((ep_expert_stream_kernel<kStreamMT, kStreamKS, true>), grid,
-                       dim3(kWave * kColWaves * kStreamKS), 0, stream, s, offset, a, as, w, ws, nullptr, q, qs);
-    return hipGetLastError();
+    return launch_product<true>(s, offset, a, as, w, ws, nullptr, q, qs, stream);
 }
 
 }  // namespace ep
