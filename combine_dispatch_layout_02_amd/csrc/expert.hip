@@ -509,34 +509,33 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
                 asm volatile("" : "+v"(acc[n][m]));   // added here, not sunk into the next block of K
             }
         };
-        i32x8 wf = weights(0);
+        // While the products with weights n run, the next weights are widened,
+        // those after next are on their way and the last products are scaled.
+        // The fences keep the scheduler from fetching everything at once.
+        auto wf = Op::make(weights(0));
+        i32x8 wraw = weights(1);
         f32x4 last[MF];
 #pragma unroll
         for (int n = 0; n < NF; ++n) {
-            // the next weights are on their way and the last products are being
-            // scaled while these are multiplied; the fence keeps the scheduler
-            // from fetching all of them at once
-            const i32x8 wnext = weights(n + 1 < NF ? n + 1 : n);
+            const i32x8 wnext = weights(n + 2 < NF ? n + 2 : NF - 1);
+            const auto wf1 = Op::make(wraw);
             f32x4 d[MF];
-            Op::multiply(Op::make(wf), xf, d);
+            Op::multiply(wf, xf, d);
+            if (n > 0) add(n - 1, last);
             between(n);
-            if constexpr (GATED) {   // no registers to spare for a second set of products
-                add(n, d);
-            } else {
-                if (n > 0) add(n - 1, last);
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // 2 reads of LDS, then in turn
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // 2 reads of LDS, then in turn
 #pragma unroll
-                for (int m = 0; m < MF; ++m) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
-                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // and 4 vector ones
-                }
-#pragma unroll
-                for (int m = 0; m < MF; ++m) last[m] = d[m];
+            for (int m = 0; m < (GATED ? 4 : 1) * MF; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // a matrix instruction
+                __builtin_amdgcn_sched_group_barrier(0x002, GATED ? 2 : 4, 0);  // and vector ones
             }
             __builtin_amdgcn_sched_barrier(0);
-            wf = wnext;
+            wf = wf1;
+            wraw = wnext;
+#pragma unroll
+            for (int m = 0; m < MF; ++m) last[m] = d[m];
         }
-        if constexpr (!GATED) add(NF - 1, last);
+        add(NF - 1, last);
     };
     // The next block's loads are issued a few at a time between the matrix
     // instructions: all at once they fill the memory pipe's queue and every
@@ -651,7 +650,7 @@ template <bool GATED>
 hipError_t launch_product(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                           const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
     const int64_t mean = s.rows / s.E;   // rows of an expert, as far as the host knows them
-    if (mean >= 64) return launch_tile<256, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+    if (mean >= 64) return launch_tile<GATED ? 192 : 256, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
     if (mean >= 24) return launch_stream<4, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
     if (mean >= 10) return launch_stream<2, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
     const int64_t blocks = (s.rows < s.E ? s.rows : s.E) * (GATED ? s.N / 128 : (s.N + 255) / 256);

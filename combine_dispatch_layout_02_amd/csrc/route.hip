@@ -22,24 +22,50 @@ namespace {
 
 constexpr int kRouteWaves = 4;   // tokens per block, one wave each (1 above 1024 experts: the groups' keys in LDS)
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int m) {
-    const int2 u = __builtin_bit_cast(int2, v);
-    return __builtin_bit_cast(double, int2{__shfl_xor(u.x, m), __shfl_xor(u.y, m)});
-}
-
 __device__ __forceinline__ double readlane_f64(double v, int lane) {
     const int2 u = __builtin_bit_cast(int2, v);
     return __builtin_bit_cast(double, int2{__builtin_amdgcn_readlane(u.x, lane), __builtin_amdgcn_readlane(u.y, lane)});
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-    for (int m = 1; m < kWave; m <<= 1) v += shfl_xor_f64(v, m);
-    return v;
+// The value of the lane that a DPP control names, `none` where there is none.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp(int none, int v) {
+    return __builtin_amdgcn_update_dpp(none, v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_f64(double v) {
+    const int2 u = __builtin_bit_cast(int2, v);
+    return __builtin_bit_cast(double, int2{dpp<CTRL, ROWS>(0, u.x), dpp<CTRL, ROWS>(0, u.y)});
 }
 
+// Reductions over the wave, returned to every lane: inside rows of 16 lanes by
+// shifts, then the rows' results carried on, the last lane's value read back.
+// Register moves only; a reduction through LDS shuffles takes five times as long.
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    v += dpp_f64<0x111, 0xf>(v);
+    v += dpp_f64<0x112, 0xf>(v);
+    v += dpp_f64<0x114, 0xf>(v);
+    v += dpp_f64<0x118, 0xf>(v);
+    v += dpp_f64<0x142, 0xa>(v);
+    v += dpp_f64<0x143, 0xc>(v);
+    return readlane_f64(v, kWave - 1);
+}
+
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+    v = max(v, (uint32_t)dpp<0x111, 0xf>(0, (int)v));
+    v = max(v, (uint32_t)dpp<0x112, 0xf>(0, (int)v));
+    v = max(v, (uint32_t)dpp<0x114, 0xf>(0, (int)v));
+    v = max(v, (uint32_t)dpp<0x118, 0xf>(0, (int)v));
+    v = max(v, (uint32_t)dpp<0x142, 0xa>(0, (int)v));
+    v = max(v, (uint32_t)dpp<0x143, 0xc>(0, (int)v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, kWave - 1);
+}
+
+// Largest of values without NaN, through unsigned integers of the same order.
 __device__ __forceinline__ float wave_max_f32(float v) {
-    for (int m = 1; m < kWave; m <<= 1) v = fmaxf(v, __shfl_xor(v, m));
-    return v;
+    const uint32_t u = f2u(v);
+    const uint32_t m = wave_max_u32((u >> 31) ? ~u : (u | 0x80000000u));
+    return u2f((m >> 31) ? (m & 0x7FFFFFFFu) : ~m);
 }
 
 __device__ __forceinline__ float load_logit(const void *z, int64_t i, bool bf16) {
@@ -62,11 +88,68 @@ __device__ __forceinline__ uint64_t order_bits(double v) {
 
 constexpr uint64_t kNone = 0x000FFFFFFFFFFFFFull;   // order_bits(-inf)
 
-// One wave per token; lane l holds experts l, l + 64, ...: EPL of them.
+__device__ __forceinline__ double order_value(uint64_t u) {
+    return __builtin_bit_cast(double, (u >> 63) ? (u & ~(1ull << 63)) : ~u);
+}
+
+// The two largest of two pairs (best >= second each).
+__device__ __forceinline__ void merge_two(double &best, double &second, double b, double s) {
+    const double low = best < b ? best : b;
+    second = second < s ? s : second;
+    second = second < low ? low : second;
+    best = best < b ? b : best;
+}
+
+// Logits of experts lane * EPL ... of a row; -inf past the last and for NaN.
+// vec: rows and base are aligned for loads of 4 elements.
+template <int EPL>
+__device__ __forceinline__ void load_logits(const void *logits, int64_t row, int E, bool bf16, bool vec, int lane,
+                                            float (&z)[EPL]) {
+    const float inf = __builtin_inff();
+    const int e0 = lane * EPL;
+    if (EPL >= 4 && vec) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+            const int e = e0 + i;
+            float v[4] = {-inf, -inf, -inf, -inf};
+            if (e < E) {   // E % 4 == 0: all four or none
+                if (bf16) {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(logits) + row + e);
+                    v[0] = bf16_lo(u.x);
+                    v[1] = bf16_hi(u.x);
+                    v[2] = bf16_lo(u.y);
+                    v[3] = bf16_hi(u.y);
+                } else {
+                    const vec16 u = ld16(static_cast<const float *>(logits) + row + e);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = u2f(u[q]);
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (i + q < EPL) z[i + q] = v[q];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) z[i] = e0 + i < E ? load_logit(logits, row + e0 + i, bf16) : -inf;
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i)
+        if (!(z[i] > -inf)) z[i] = -inf;
+}
+
+// One wave per token; lane l holds experts l EPL ... l EPL + EPL - 1, so that
+// the lowest lane, then the lowest place, is the lowest index.  What bounds a
+// small batch is the chain of dependent steps in a wave, so the reductions are
+// register moves: the largest upper halves of the keys by a maximum over the
+// wave, ties by the lower halves, the first lane of those left by a ballot.
+// (One token, 256 experts, 8 groups: 11.0 us with reductions through LDS
+// shuffles and the groups scanned from LDS, EP_ROUTE_US us so.)
 template <int EPL>
 __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_kernel(Router r, const void *logits, const float *bias,
-                                                                    int64_t *topk_idx, float *topk_w) {
-    extern __shared__ double group_keys[];   // [waves][E] keys, when there are groups
+                                                                    int64_t *topk_idx, float *topk_w, bool vec) {
+    constexpr bool KEEP = EPL <= 16;         // scores stay in registers for the weights
+    extern __shared__ double group_keys[];   // [waves][E] keys, for groups that lanes do not split evenly
     const int lane = threadIdx.x & (kWave - 1);
     const int64_t t = (int64_t)blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave;
     if (t >= r.T) return;   // wave-uniform; waves share nothing
@@ -74,113 +157,146 @@ __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_kernel(Router r, co
     const float inf = __builtin_inff();
 
     float z[EPL];
+    load_logits(logits, row, r.E, r.bf16, vec, lane, z);
     float top = -inf;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-        const int e = i * kWave + lane;
-        z[i] = e < r.E ? load_logit(logits, row + e, r.bf16) : -inf;
-        if (!(z[i] > -inf)) z[i] = -inf;   // NaN too
-        top = fmaxf(top, z[i]);
-    }
     double total = 1.0;
+    double p[KEEP ? EPL : 1];   // sigmoid, or e^(z - top)
     if (r.softmax) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) top = fmaxf(top, z[i]);
         top = wave_max_f32(top);
         double s = 0.0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s += z[i] == -inf ? 0.0 : exp_below(z[i], top);
+        for (int i = 0; i < EPL; ++i) {
+            const double v = z[i] == -inf ? 0.0 : exp_below(z[i], top);
+            if (KEEP) p[KEEP ? i : 0] = v;
+            s += v;
+        }
         total = wave_sum_f64(s);
     }
     uint64_t key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-        const int e = i * kWave + lane;
-        key[i] = kNone;
-        if (z[i] == -inf) continue;
-        double v = r.softmax ? exp_below(z[i], top) / total : sigmoid_f64(z[i]);
-        if (bias) v += (double)bias[e];
-        if (v == v) key[i] = order_bits(v);
+        const int e = lane * EPL + i;
+        double v;
+        if (r.softmax)
+            v = (KEEP ? p[KEEP ? i : 0] : exp_below(z[i], top)) / total;
+        else
+            v = sigmoid_f64(z[i]);
+        if (KEEP && !r.softmax) p[KEEP ? i : 0] = v;
+        if (bias && e < r.E) v += (double)bias[e];
+        key[i] = (z[i] == -inf || !(v == v)) ? kNone : order_bits(v);
     }
 
     if (r.G > 1) {
-        double *mine = group_keys + (size_t)(threadIdx.x / kWave) * r.E;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = i * kWave + lane;
-            const uint64_t u = key[i];
-            if (e < r.E) mine[e] = __builtin_bit_cast(double, (u >> 63) ? (u & ~(1ull << 63)) : ~u);
-        }
-        __builtin_amdgcn_wave_barrier();
-        const int per = r.E / r.G;
+        const int per = r.E / r.G, span = per / EPL;   // experts and lanes of a group
         double best = -(double)inf, second = -(double)inf;
-        if (lane < r.G)
-            for (int i = 0; i < per; ++i) {
-                const double v = mine[lane * per + i];
-                if (v > best) {
-                    second = best;
-                    best = v;
-                } else if (v > second) {
-                    second = v;
-                }
-            }
-        double mark = r.gtop == 2 ? best + second : best;
-        if (lane >= r.G || !(mark == mark)) mark = -(double)inf;
-        int before = 0;   // groups ahead of this lane's: larger, or as large and earlier
-        for (int g = 0; g < r.G; ++g) {
-            const double other = readlane_f64(mark, g);
-            before += (other > mark || (other == mark && g < lane)) ? 1 : 0;
-        }
-        const uint64_t keep = __ballot(lane < r.G && before < r.Gk);
+        const bool even = per % EPL == 0 && (span & (span - 1)) == 0 && span <= 16;
+        int home;          // a lane that holds group `lane`'s mark
+        if (even) {        // groups are runs of 1, 2, 4, 8 or 16 lanes
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-            const int e = i * kWave + lane;
-            if (e < r.E && !((keep >> (e / per)) & 1)) key[i] = kNone;
+            for (int i = 0; i < EPL; ++i) {
+                const double v = order_value(key[i]);
+                second = v > best ? best : (v > second ? v : second);
+                best = v > best ? v : best;
+            }
+            if (span > 1) merge_two(best, second, dpp_f64<0xB1, 0xf>(best), dpp_f64<0xB1, 0xf>(second));    // lane ^ 1
+            if (span > 2) merge_two(best, second, dpp_f64<0x4E, 0xf>(best), dpp_f64<0x4E, 0xf>(second));    // lane ^ 2
+            if (span > 4) merge_two(best, second, dpp_f64<0x141, 0xf>(best), dpp_f64<0x141, 0xf>(second));  // 8 reversed
+            if (span > 8) merge_two(best, second, dpp_f64<0x140, 0xf>(best), dpp_f64<0x140, 0xf>(second));  // 16 reversed
+            home = span;
+        } else {
+            double *mine = group_keys + (size_t)(threadIdx.x / kWave) * r.E;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (lane * EPL + i < r.E) mine[lane * EPL + i] = order_value(key[i]);
+            __builtin_amdgcn_wave_barrier();
+            if (lane < r.G)
+                for (int i = 0; i < per; ++i) {
+                    const double v = mine[lane * per + i];
+                    second = v > best ? best : (v > second ? v : second);
+                    best = v > best ? v : best;
+                }
+            home = 1;
+        }
+        double mark = r.gtop == 2 ? best + second : best;
+        if (!(mark == mark)) mark = -(double)inf;
+        // this lane's group, and the groups ahead of it: larger, or as large and earlier
+        const int mine = lane / home;
+        int before = 0;
+        for (int g = 0; g < r.G; ++g) {
+            const double other = readlane_f64(mark, g * home);
+            before += (other > mark || (other == mark && g < mine)) ? 1 : 0;
+        }
+        const bool kept = mine < r.G && before < r.Gk;
+        if (even) {
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+                if (!kept) key[i] = kNone;
+        } else {
+            const uint64_t keep = __ballot(kept);   // bit g: group g
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) {
+                const int e = lane * EPL + i;
+                if (e < r.E && !((keep >> (e / per)) & 1)) key[i] = kNone;
+            }
         }
     }
 
-    int taken = -1;   // lane j: the j-th expert
+    int taken = -1;           // lane j: the j-th expert
+    double score = 0.0;       // and its p
     for (int j = 0; j < r.k; ++j) {
-        uint64_t b = kNone;
-        int be = r.E;
+        uint64_t b = key[0];
+        int at = 0;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
+        for (int i = 1; i < EPL; ++i)
             if (key[i] > b) {
                 b = key[i];
-                be = i * kWave + lane;
+                at = i;
             }
-#pragma unroll
-        for (int m = 1; m < kWave; m <<= 1) {
-            const uint64_t ob = ((uint64_t)(uint32_t)__shfl_xor((int)(b >> 32), m) << 32) |
-                                (uint32_t)__shfl_xor((int)(uint32_t)b, m);
-            const int oe = __shfl_xor(be, m);
-            if (ob > b || (ob == b && oe < be)) {
-                b = ob;
-                be = oe;
-            }
+        const uint32_t hi = wave_max_u32((uint32_t)(b >> 32));
+        if (hi == (uint32_t)(kNone >> 32)) break;   // nothing is left (no number but -inf has these bits)
+        uint64_t first = __ballot((uint32_t)(b >> 32) == hi);
+        if (first & (first - 1)) {   // several: the largest lower half, then the first lane
+            const uint32_t lo = wave_max_u32((uint32_t)(b >> 32) == hi ? (uint32_t)b : 0u);
+            first &= __ballot((uint32_t)b == lo);
         }
-        if (b <= kNone) break;   // the same in every lane
-        if (lane == j) taken = be;
+        const int winner = __builtin_ctzll(first);
+        const int place = __builtin_amdgcn_readlane(at, winner);
+        if (KEEP) {
+            double mine = p[0];
+#pragma unroll
+            for (int i = 1; i < EPL; ++i)
+                if (at == i) mine = p[KEEP ? i : 0];
+            const double v = readlane_f64(mine, winner);
+            if (lane == j) score = v;
+        }
+        if (lane == j) taken = winner * EPL + place;
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-            if (be == i * kWave + lane) key[i] = kNone;
+            if (lane == winner && i == place) key[i] = kNone;
     }
 
     // the weights, slot j in lane j
-    const float zt = taken >= 0 ? load_logit(logits, row + taken, r.bf16) : -inf;
-    const float chosen_top = wave_max_f32(zt);
-    double p;
-    if (!r.softmax)
-        p = taken >= 0 ? sigmoid_f64(zt) : 0.0;
-    else if (r.renorm)   // a softmax over the taken experts alone: the common sum cancels
-        p = taken >= 0 ? exp_below(zt, chosen_top) : 0.0;
-    else
-        p = taken >= 0 ? exp_below(zt, top) / total : 0.0;
-    if (r.renorm) {
-        const double sum = wave_sum_f64(p);
-        p = sum > 0.0 ? p / sum : 0.0;
+    if (!KEEP && taken >= 0) {
+        const float zt = load_logit(logits, row + taken, r.bf16);
+        score = r.softmax ? exp_below(zt, top) : sigmoid_f64(zt);
     }
+    double weight = r.softmax ? score / total : score;
+    if (r.renorm) {   // the softmax's common sum cancels
+        double sum = wave_sum_f64(score);
+        if (r.softmax && !(sum > 0.0)) {   // the taken experts' scores all vanish against the largest
+            const float zt = taken >= 0 ? load_logit(logits, row + taken, r.bf16) : -inf;
+            const float m = wave_max_f32(zt);
+            score = taken >= 0 ? exp_below(zt, m) : 0.0;
+            sum = wave_sum_f64(score);
+        }
+        weight = sum > 0.0 ? score / sum : 0.0;
+    }
+    if (taken < 0) weight = 0.0;
     if (lane < r.k) {
         topk_idx[t * r.k + lane] = taken;
-        topk_w[t * r.k + lane] = (float)(p * (double)r.scale);
+        topk_w[t * r.k + lane] = (float)(weight * (double)r.scale);
     }
 }
 
@@ -292,11 +408,12 @@ hipError_t with_epl(int E, F f) {
 hipError_t launch_route(const Router &r, const void *logits, const float *bias, int64_t *topk_idx,
                         float *topk_w, hipStream_t stream) {
     const int waves = r.E > 1024 ? 1 : kRouteWaves;
+    const bool vec = r.E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
     const size_t lds = r.G > 1 ? sizeof(double) * (size_t)waves * r.E : 0;   // at most 32 KiB
     const dim3 grid((unsigned)((r.T + waves - 1) / waves)), block(kWave * waves);
     return with_epl(r.E, [&](auto epl) {
         hipLaunchKernelGGL(ep_route_kernel<decltype(epl)::value>, grid, block, lds, stream, r, logits, bias, topk_idx,
-                           topk_w);
+                           topk_w, vec);
         return hipGetLastError();
     });
 }

@@ -585,12 +585,30 @@ def make_router(E, k, score="softmax", num_groups=1, topk_groups=None, group_top
                      0, float(scale))
 
 
-def _on_current(*tensors):
-    """Every tensor given lives on the current device (the launch goes there)."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else None
+def _here(*tensors):
+    """Pointers of tensors (or None) of the current device, which the launch goes to."""
+    dev, out = -1, []
     for t in tensors:
-        if t is not None and t.is_cuda and t.get_device() != dev:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError("device tensor expected")
+        if dev < 0:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
             raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError("contiguous tensor expected")
+        out.append(t.data_ptr() or None)
+    return out
+
+
+def _on(stream):
+    """The raw handle of a stream, by default the current device's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _router_for(router, logits):
@@ -611,9 +629,8 @@ def ep_route(router, logits, bias, topk_idx, topk_w, stream=None):
         _need(bias, torch.float32, (r.num_experts,), "bias")
     _need(topk_idx, torch.int64, (T, k), "topk_idx")
     _need(topk_w, torch.float32, (T, k), "topk_w")
-    _on_current(logits, bias, topk_idx, topk_w)
-    _ok(load().ep_route(ctypes.byref(r), T, _ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(topk_w),
-                        _stream(stream)), "ep_route")
+    ptrs = _here(logits, bias, topk_idx, topk_w)
+    _ok(load().ep_route(ctypes.byref(r), T, *ptrs, _on(stream)), "ep_route")
 
 
 def ep_route_backward(router, logits, topk_idx, grad_topk_w, grad_logits, stream=None):
@@ -623,9 +640,8 @@ def ep_route_backward(router, logits, topk_idx, grad_topk_w, grad_logits, stream
     _need(topk_idx, torch.int64, (T, k), "topk_idx")
     _need(grad_topk_w, torch.float32, (T, k), "grad_topk_w")
     _need(grad_logits, logits.dtype, logits.shape, "grad_logits")
-    _on_current(logits, topk_idx, grad_topk_w, grad_logits)
-    _ok(load().ep_route_backward(ctypes.byref(r), T, _ptr(logits), _ptr(topk_idx), _ptr(grad_topk_w),
-                                 _ptr(grad_logits), _stream(stream)), "ep_route_backward")
+    ptrs = _here(logits, topk_idx, grad_topk_w, grad_logits)
+    _ok(load().ep_route_backward(ctypes.byref(r), T, *ptrs, _on(stream)), "ep_route_backward")
 
 
 def _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity) -> ep_expert_shape:
@@ -638,7 +654,6 @@ def _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_ca
     _need(a_scales, torch.float32, (rows, K // 128), "a_scales")
     _need(w, torch.uint8, (E, wide, K), "w")
     _need(w_scales, torch.float32, (E, (wide + 127) // 128, K // 128), "w_scales")
-    _on_current(expert_offset, a, a_scales, w, w_scales)
     return ep_expert_shape(rows, E, K, N, int(num_ranks), int(rank_capacity))
 
 
@@ -648,9 +663,8 @@ def ep_expert_gemm(expert_offset, a, a_scales, w, w_scales, out, num_ranks=1, ra
     N = w.shape[1]
     sh = _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity)
     _need(out, torch.bfloat16, (sh.rows, N), "out")
-    _on_current(out)
-    _ok(load().ep_expert_gemm(ctypes.byref(sh), _ptr(expert_offset), _ptr(a), _ptr(a_scales), _ptr(w),
-                              _ptr(w_scales), _ptr(out), _stream(stream)), "ep_expert_gemm")
+    ptrs = _here(expert_offset, a, a_scales, w, w_scales, out)
+    _ok(load().ep_expert_gemm(ctypes.byref(sh), *ptrs, _on(stream)), "ep_expert_gemm")
 
 
 def ep_expert_gated(expert_offset, a, a_scales, w, w_scales, out_q, out_scales, num_ranks=1, rank_capacity=0,
@@ -663,23 +677,21 @@ def ep_expert_gated(expert_offset, a, a_scales, w, w_scales, out_q, out_scales, 
     sh = _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity)
     _need(out_q, torch.uint8, (sh.rows, N), "out_q")
     _need(out_scales, torch.float32, (sh.rows, N // 128), "out_scales")
-    _on_current(out_q, out_scales)
-    _ok(load().ep_expert_gated(ctypes.byref(sh), _ptr(expert_offset), _ptr(a), _ptr(a_scales), _ptr(w),
-                               _ptr(w_scales), _ptr(out_q), _ptr(out_scales), _stream(stream)), "ep_expert_gated")
+    ptrs = _here(expert_offset, a, a_scales, w, w_scales, out_q, out_scales)
+    _ok(load().ep_expert_gated(ctypes.byref(sh), *ptrs, _on(stream)), "ep_expert_gated")
 
 
 def ep_combine_backward(shape, dy, expert_out, token_slot, topk_w, grad_expert_out, grad_topk_w, stream=None):
     """Gradients of ep_combine (bf16 payload) over expert_out and topk_w."""
-    T, k, H = shape.num_tokens, shape.num_topk, shape.hidden
+    T, k, H, rows = shape.num_tokens, shape.num_topk, shape.hidden, shape.rows
     _need(dy, torch.bfloat16, (T, H), "dy")
-    _need(expert_out, torch.bfloat16, (shape.rows, H), "expert_out")
+    _need(expert_out, torch.bfloat16, (rows, H), "expert_out")
     _need(token_slot, torch.int32, (T, k), "token_slot")
     _need(topk_w, torch.float32, (T, k), "topk_w")
-    _need(grad_expert_out, torch.bfloat16, (shape.rows, H), "grad_expert_out")
+    _need(grad_expert_out, torch.bfloat16, (rows, H), "grad_expert_out")
     _need(grad_topk_w, torch.float32, (T, k), "grad_topk_w")
-    _on_current(dy, expert_out, token_slot, topk_w, grad_expert_out, grad_topk_w)
-    _ok(load().ep_combine_backward(ctypes.byref(shape), _ptr(dy), _ptr(expert_out), _ptr(token_slot), _ptr(topk_w),
-                                   _ptr(grad_expert_out), _ptr(grad_topk_w), _stream(stream)), "ep_combine_backward")
+    ptrs = _here(dy, expert_out, token_slot, topk_w, grad_expert_out, grad_topk_w)
+    _ok(load().ep_combine_backward(ctypes.byref(shape), *ptrs, _on(stream)), "ep_combine_backward")
 
 
 def ep_accounting(shape, own_node, num_tokens_per_rank, num_tokens_per_node, rdma_algo_token_count,
@@ -880,41 +892,46 @@ def combine_ranks(partial, handle: RankHandle, stream=None):
 
 # --------------------------------------------------------------------------- router, experts, gradients (allocating)
 
+def _alloc(like, *outs, stream=None):
+    """Uninitialised tensors (shape, dtype) beside `like`, from the memory of the stream they are written on."""
+    if stream is None:
+        return [like.new_empty(shape, dtype=dtype) for shape, dtype in outs]
+    with torch.cuda.stream(stream):
+        return [like.new_empty(shape, dtype=dtype) for shape, dtype in outs]
+
+
 def route(logits, router, bias=None, stream=None):
     """Returns topk_idx (int64, -1: no expert left) and topk_w (fp32), both [T, k]: what dispatch takes."""
-    T, k = logits.shape[0], router.num_topk
-    idx = torch.empty((T, k), dtype=torch.int64, device=logits.device)
-    w = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    shape = (logits.shape[0], router.num_topk)
+    idx, w = _alloc(logits, (shape, torch.int64), (shape, torch.float32), stream=stream)
     ep_route(router, logits, bias, idx, w, stream)
     return idx, w
 
 
 def route_backward(grad_topk_w, logits, topk_idx, router, stream=None):
     """Gradient over the logits of route's weights."""
-    g = torch.empty_like(logits)
+    g, = _alloc(logits, (logits.shape, logits.dtype), stream=stream)
     ep_route_backward(router, logits, topk_idx, grad_topk_w, g, stream)
     return g
 
 
 def expert_gemm(expert_offset, a, a_scales, w, w_scales, num_ranks=1, rank_capacity=0, stream=None):
     """bf16 rows [rows, N]; rows of no segment hold whatever the allocation held."""
-    out = torch.empty((a.shape[0], w.shape[1]), dtype=torch.bfloat16, device=a.device)
+    out, = _alloc(a, ((a.shape[0], w.shape[1]), torch.bfloat16), stream=stream)
     ep_expert_gemm(expert_offset, a, a_scales, w, w_scales, out, num_ranks, rank_capacity, stream)
     return out
 
 
 def expert_gated(expert_offset, a, a_scales, w, w_scales, num_ranks=1, rank_capacity=0, stream=None):
     """FP8_S128 rows: e4m3 [rows, N] and scales [rows, N/128]; rows of no segment as the allocation held them."""
-    N = w.shape[1] // 2
-    q = torch.empty((a.shape[0], N), dtype=torch.uint8, device=a.device)
-    s = torch.empty((a.shape[0], N // 128), dtype=torch.float32, device=a.device)
+    rows, N = a.shape[0], w.shape[1] // 2
+    q, s = _alloc(a, ((rows, N), torch.uint8), ((rows, N // 128), torch.float32), stream=stream)
     ep_expert_gated(expert_offset, a, a_scales, w, w_scales, q, s, num_ranks, rank_capacity, stream)
     return q, s
 
 
 def combine_backward(dy, expert_out, handle: Handle, stream=None):
     """Returns grad_expert_out [rows, H] bf16 (rows of no slot as the allocation held them) and grad_topk_w [T, k]."""
-    g = torch.empty_like(expert_out)
-    gw = torch.empty_like(handle.topk_w)
+    g, gw = _alloc(expert_out, (expert_out.shape, torch.bfloat16), (handle.topk_w.shape, torch.float32), stream=stream)
     ep_combine_backward(handle.shape, dy, expert_out, handle.token_slot, handle.topk_w, g, gw, stream)
     return g, gw
