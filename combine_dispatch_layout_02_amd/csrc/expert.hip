@@ -71,6 +71,10 @@ struct Operand<false> {
 #pragma unroll
         for (int m = 0; m < MT; ++m) d[m] = mfma_128(a, b[m]);
     }
+    static __device__ __forceinline__ void multiply(const type (&a)[2], const type &b, f32x4 (&d)[2]) {
+        d[0] = mfma_128(a[0], b);
+        d[1] = mfma_128(a[1], b);
+    }
 };
 template <>
 struct Operand<true> {
@@ -83,6 +87,13 @@ struct Operand<true> {
         for (int k = 0; k < 4; ++k)
 #pragma unroll
             for (int m = 0; m < MT; ++m) d[m] = mfma_32(a.v[k], b[m].v[k], k ? d[m] : zero);
+    }
+    static __device__ __forceinline__ void multiply(const type (&a)[2], const type &b, f32x4 (&d)[2]) {
+        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int f = 0; f < 2; ++f) d[f] = mfma_32(a[f].v[k], b.v[k], k ? d[f] : zero);
     }
 };
 
@@ -189,23 +200,27 @@ constexpr int kColWaves = 8;   // waves side by side: 16 weight rows twice each
 // blocks in flight and no barrier.  The rows of a are shared by the waves: XB
 // blocks of K at a time, two buffers, a barrier per change.
 template <int MT, int KS, bool GATED>
-__global__ __launch_bounds__(64 * kColWaves * KS, MT == 4 ? 2 : 4) void ep_expert_stream_kernel(
+__global__ __attribute__((amdgpu_waves_per_eu(4, 4)))
+__launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
     uint16_t *out, uint8_t *oq, float *oqs, int cols) {
-    constexpr int XB = MT == 4 ? 1 : 2;              // blocks of K of a's rows per change
-    constexpr int XBYTES = 16 * MT * 128 * XB;       // 4 or 8 KiB: a piece of XBYTES / 8 per wave
+    constexpr int XB = 2;                        // blocks of K of a's rows per change
+    constexpr int XBYTES = 16 * MT * 128 * XB;   // 4 or 8 KiB
     __shared__ __attribute__((aligned(16))) uint8_t wbuf0[kColWaves * KS * 4096];
     __shared__ __attribute__((aligned(16))) uint8_t wbuf1[kColWaves * KS * 4096];
     __shared__ __attribute__((aligned(16))) uint8_t xbuf0[KS * XBYTES];
     __shared__ __attribute__((aligned(16))) uint8_t xbuf1[KS * XBYTES];
-    __shared__ int found;
-    __shared__ float amax[GATED ? kColWaves : 1][GATED ? 16 * MT : 1];
+    // two blocks share a CU's 160 KiB to the byte: the tile's expert and the
+    // groups' maxima use the buffers before and after
+    int *found = reinterpret_cast<int *>(xbuf0);
+    float (*amax)[16 * MT] = reinterpret_cast<float (*)[16 * MT]>(wbuf1);
     typedef Operand<GATED> Op;
     int e, row, end;
     // columns first: an expert's blocks spread over the XCDs, also where only a
     // few experts have rows
     const int ct = blockIdx.x % cols;
-    if (!find_tile(off, s, blockIdx.x / cols, 16 * MT, &found, &e, &row, &end)) return;
+    if (!find_tile(off, s, blockIdx.x / cols, 16 * MT, found, &e, &row, &end)) return;
+    __syncthreads();   // everyone has read it
 
     const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int col = wid % kColWaves, ks = wid / kColWaves;
@@ -278,27 +293,25 @@ __global__ __launch_bounds__(64 * kColWaves * KS, MT == 4 ? 2 : 4) void ep_exper
         }
         const uint8_t *wp = wbuf + wid * 4096;
         const i32x8 f0 = lds_operand(wp + plo, wp + phi), f1 = lds_operand(wp + 2048 + plo, wp + 2048 + phi);
-        const uint8_t *xp = xbuf + ks * XBYTES + part * (16 * MT * 128);
-        i32x8 xr[MT];
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xr[m] = lds_operand(xp + 2048 * m + plo, xp + 2048 * m + phi);
+        const typename Op::type wf[2] = {Op::make(f0), Op::make(f1)};
         // the operands are in registers: their place takes the block after next
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
         __builtin_amdgcn_sched_barrier(0);
         stage_w(wbuf, i + 2);
         __builtin_amdgcn_sched_barrier(0);
-        typename Op::type x[MT];
+        const uint8_t *xp = xbuf + ks * XBYTES + part * (16 * MT * 128);
+        i32x8 xr = lds_operand(xp + plo, xp + phi);
 #pragma unroll
-        for (int m = 0; m < MT; ++m) x[m] = Op::make(xr[m]);
+        for (int m = 0; m < MT; ++m) {   // one group of rows at a time: few registers, two blocks to a CU
+            const auto x = Op::make(xr);
+            if (m + 1 < MT) xr = lds_operand(xp + 2048 * (m + 1) + plo, xp + 2048 * (m + 1) + phi);
+            f32x4 d[2];
+            Op::multiply(wf, x, d);
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            f32x4 d[MT];
-            Op::multiply(Op::make(f ? f1 : f0), x, d);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
+            for (int f = 0; f < 2; ++f) {
                 const float sc = cx[m][j] * cw[f][j];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) acc[f][m][q] = __builtin_fmaf(d[m][q], sc, acc[f][m][q]);
+                for (int q = 0; q < 4; ++q) acc[f][m][q] = __builtin_fmaf(d[f][q], sc, acc[f][m][q]);
                 asm volatile("" : "+v"(acc[f][m]));   // added here, not after the next loads
             }
         }
@@ -370,6 +383,7 @@ __global__ __launch_bounds__(64 * kColWaves * KS, MT == 4 ? 2 : 4) void ep_exper
         }
     } else {
         f32x4 h[MT];
+        float tops[MT];
         if (ks == 0) {
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
@@ -380,10 +394,13 @@ __global__ __launch_bounds__(64 * kColWaves * KS, MT == 4 ? 2 : 4) void ep_exper
                     top = fmaxf(top, fabsf(h[m][i]));
                 }
                 top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                if (quad == 0) amax[col][16 * m + r16] = top;
+                tops[m] = fmaxf(top, __shfl_xor(top, 32));
             }
         }
+        __syncthreads();   // nobody reads the buffers any more
+        if (ks == 0 && quad == 0)
+#pragma unroll
+            for (int m = 0; m < MT; ++m) amax[col][16 * m + r16] = tops[m];
         __syncthreads();
         if (ks > 0) return;
 #pragma unroll
@@ -408,19 +425,21 @@ __global__ __launch_bounds__(64 * kColWaves * KS, MT == 4 ? 2 : 4) void ep_exper
 constexpr int kTileThreads = 512, kTileN = 256;   // 8 waves; weight rows of a tile
 
 // One block: BM rows by 256 weight rows (gated: 128 gate rows and the matching
-// 128 up rows), 8 waves, WN of them side by side.  Both operands of a block of
-// K = 128 are staged in LDS, two buffers in turn: the next block's loads are
-// in flight while this one is multiplied.
-template <int BM, int WN, bool GATED>
+// 128 up rows), 8 waves, 2 by 4.  Both operands of a block of K = 128 are
+// staged in LDS, 2 or 3 buffers in turn: the next blocks' loads are in flight
+// while this one is multiplied.
+template <int BM, bool GATED>
 __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
     uint16_t *out, uint8_t *oq, float *oqs, int slots, int cols) {
-    constexpr int WM = 8 / WN, NF = kTileN / WN / 16, MF = BM / WM / 16;
+    constexpr int WN = 2, WM = 4, NF = kTileN / WN / 16, MF = BM / WM / 16;
+    constexpr int STAGES = BM <= 128 ? 3 : 2;      // what fits 160 KiB of LDS
     constexpr int HALF = GATED ? 2 : 1;            // gate and up, or one product
     constexpr int WCOLS = kTileN / HALF / WN;      // columns of the result per wave
     typedef Operand<GATED> Op;
     __shared__ __attribute__((aligned(16))) uint8_t buf0[(kTileN + BM) * 128];
     __shared__ __attribute__((aligned(16))) uint8_t buf1[(kTileN + BM) * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[STAGES == 3 ? (kTileN + BM) * 128 : 16];
     __shared__ int found;
     __shared__ float amax[GATED ? WN : 1][GATED ? BM : 1];
 
@@ -460,13 +479,15 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     const rsrc_t xb = buffer(a + (size_t)row * s.K);
 
     constexpr int PIECES = (kTileN + BM) / 64;
+    static_assert(PIECES <= 15, "the waits' counts");
     const auto stage = [&](uint8_t *buf, int kb, int p) {   // piece p of a block of K
+        const uint32_t past = kb < KB ? 0u : 0x80000000u;
         if (GATED && p < kTileN / 64)
-            load_to_lds(p < 2 ? wb0 : wb1, buf + p * 8192 + wid * 1024, woff[0], (p & 1) * 64 * s.K + kb * 128);
+            load_to_lds(p < 2 ? wb0 : wb1, buf + p * 8192 + wid * 1024, woff[0] | past, (p & 1) * 64 * s.K + kb * 128);
         else if (p < kTileN / 64)
-            load_to_lds(wb0, buf + p * 8192 + wid * 1024, woff[p], kb * 128);
+            load_to_lds(wb0, buf + p * 8192 + wid * 1024, woff[p] | past, kb * 128);
         else
-            load_to_lds(xb, buf + p * 8192 + wid * 1024, xoff[p - kTileN / 64], kb * 128);
+            load_to_lds(xb, buf + p * 8192 + wid * 1024, xoff[p - kTileN / 64] | past, kb * 128);
     };
 
     // scales: one register per lane and group of 16 rows, one (or gate's and
@@ -537,31 +558,38 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
         }
         add(NF - 1, last);
     };
-    // The next block's loads are issued a few at a time between the matrix
-    // instructions: all at once they fill the memory pipe's queue and every
-    // wave waits at the start of the block.  The last block loads itself again
-    // (a branch here would cost registers).
+    // The loads of the block STAGES - 1 on are issued a few at a time between
+    // the matrix instructions: all at once they fill the memory pipe's queue and
+    // every wave waits.  Past the last block they read past the buffer's end
+    // (zeros, no memory traffic), which keeps the counts of the waits.
     const auto step = [&](const uint8_t *cur, uint8_t *next, int kb) {
+        // this wave's part of the block has arrived, of what came later at most
+        // the loads of STAGES - 2 blocks are under way; then every wave's part,
+        // and the buffer of the block before is free
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (STAGES - 2) * PIECES);
+        barrier_only();
         float x[MF], c[HALF];
 #pragma unroll
         for (int m = 0; m < MF; ++m) x[m] = sx[m];
 #pragma unroll
         for (int h = 0; h < HALF; ++h) c[h] = sw[h];
-        __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): this wave's part of the block has arrived
-        __syncthreads();                      // every wave's part; and the other buffer is free
-        const int after = min(kb + 1, KB - 1);
-        scales(after);
+        scales(min(kb + 1, KB - 1));
+        __builtin_amdgcn_sched_barrier(0);
         multiply(cur, x, c, [&](int n) {
 #pragma unroll
-            for (int p = n * PIECES / NF; p < (n + 1) * PIECES / NF; ++p) stage(next, after, p);
+            for (int p = n * PIECES / NF; p < (n + 1) * PIECES / NF; ++p) stage(next, kb + STAGES - 1, p);
         });
     };
+    scales(0);
 #pragma unroll
     for (int p = 0; p < PIECES; ++p) stage(buf0, 0, p);
-    scales(0);
-    for (int kb = 0; kb < KB; kb += 2) {
-        step(buf0, buf1, kb);
+    if (STAGES == 3)
+#pragma unroll
+        for (int p = 0; p < PIECES; ++p) stage(buf1, 1, p);
+    for (int kb = 0; kb < KB; kb += STAGES) {
+        step(buf0, STAGES == 3 ? buf2 : buf1, kb);
         if (kb + 1 < KB) step(buf1, buf0, kb + 1);
+        if (STAGES == 3 && kb + 2 < KB) step(buf2, buf1, kb + 2);
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);
 
@@ -627,12 +655,12 @@ bool expert_grid_fits(const ExpertShape &s, bool gated) {
 
 namespace {
 
-template <int BM, int WN, bool GATED>
+template <int BM, bool GATED>
 hipError_t launch_tile(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                        const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
     const int slots = (int)tile_slots(s, BM), cols = GATED ? s.N / 128 : (s.N + kTileN - 1) / kTileN;
     const int64_t blocks = (int64_t)((slots + 7) / 8) * 8 * cols;
-    hipLaunchKernelGGL((ep_expert_tile_kernel<BM, WN, GATED>), dim3((unsigned)blocks), dim3(kTileThreads), 0, stream,
+    hipLaunchKernelGGL((ep_expert_tile_kernel<BM, GATED>), dim3((unsigned)blocks), dim3(kTileThreads), 0, stream,
                        s, offset, a, as, w, ws, out, q, qs, slots, cols);
     return hipGetLastError();
 }
@@ -646,16 +674,36 @@ hipError_t launch_stream(const ExpertShape &s, const int32_t *offset, const uint
     return hipGetLastError();
 }
 
+// Which form: by the rows of an expert on average, all that the host knows of
+// them, and by whether the tiles fill the 256 CUs.  Measured on uniform routing
+// over 32 experts, K = 7168 and 4096 (gated) or 2048 weight rows, and over 96
+// experts, K = 1024 and 768 or 384 weight rows (us):
+//   mean rows           8 (32)  32 (32)  128 (32)  256 (32)  1024 (32)  171 (96)
+//   gated   32 rows       177      215       428       713       2460        92
+//          192 rows       378      440       460       759       2027        65
+//   product 32 rows       111      117       196       315       1052        42
+//          128 rows       120      153       185       252        832        32
+//          256 rows       124      206       138       287        691        25
+// (96 experts at mean 43, product: 18.1, 14.6 and 20.1.)  One token over 8 of
+// 32 experts leaves 128 blocks (gated): K split over 2 groups of waves 60 us,
+// one group 92 us.
 template <bool GATED>
 hipError_t launch_product(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                           const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
-    const int64_t mean = s.rows / s.E;   // rows of an expert, as far as the host knows them
-    if (mean >= 64) return launch_tile<GATED ? 192 : 256, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
-    if (mean >= 24) return launch_stream<4, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
-    if (mean >= 10) return launch_stream<2, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
-    const int64_t blocks = (s.rows < s.E ? s.rows : s.E) * (GATED ? s.N / 128 : (s.N + 255) / 256);
-    if (blocks >= 512) return launch_stream<1, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
-    return launch_stream<1, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+    const int64_t mean = s.rows / s.E, cols = GATED ? s.N / 128 : (s.N + 255) / 256;
+    const auto tiles = [&](int BM) { return (s.rows / BM + 1) * cols; };
+    if constexpr (GATED) {
+        if (mean >= 160 && tiles(192) >= 192)
+            return launch_tile<192, true>(s, offset, a, as, w, ws, out, q, qs, stream);
+    } else {
+        if (mean >= 96 && tiles(256) >= 192)
+            return launch_tile<256, false>(s, offset, a, as, w, ws, out, q, qs, stream);
+        if (mean >= 40 && tiles(128) >= 192)
+            return launch_tile<128, false>(s, offset, a, as, w, ws, out, q, qs, stream);
+    }
+    if (mean < 16 && (s.rows < s.E ? s.rows : s.E) * cols < 512)
+        return launch_stream<1, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+    return launch_stream<2, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
 }
 
 }  // namespace
