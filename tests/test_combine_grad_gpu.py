@@ -139,3 +139,10 @@ def test_no_tokens(ep):
     h = ep.Handle(shape, e(0, 2, d=torch.int32), None, e(0, 2, d=torch.float32))
     g, gw = ep.combine_backward(e(0, 64), e(0, 64), h)
     assert g.shape == (0, 64) and gw.shape == (0, 2)
+
+
+@pytest.mark.parametrize("T,H,k", [(1024, 264, 3), (1100, 2056, 4), (1500, 40, 9)])
+def test_one_wave_a_token(ep, T, H, k):
+    rng = np.random.default_rng(T)
+    shape = ep.make_shape(T, H, 64, 4, 1, k)
+    _check(ep, shape, *_inputs(rng, T, H, k, T * k, 0.1))
