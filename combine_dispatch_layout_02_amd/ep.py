@@ -585,30 +585,26 @@ def make_router(E, k, score="softmax", num_groups=1, topk_groups=None, group_top
                      0, float(scale))
 
 
-def _here(*tensors):
-    """Pointers of tensors (or None) of the current device, which the launch goes to."""
-    dev, out = -1, []
+def _here(stream, *tensors):
+    """Pointers of tensors (or None) and the stream's raw handle, all of the
+    current device: the launch goes there.  None: its current stream."""
+    if not tensors[0].is_cuda:
+        raise ValueError("device tensor expected")
+    dev = torch.cuda.current_device()
     for t in tensors:
-        if t is None:
-            out.append(None)
-            continue
-        if not t.is_cuda:
-            raise ValueError("device tensor expected")
-        if dev < 0:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            if not t.is_cuda:
+                raise ValueError("device tensor expected")
+            if not t.is_contiguous():
+                raise ValueError("contiguous tensor expected")
             raise ValueError(f"tensor on cuda:{t.get_device()}, the current device is cuda:{dev}")
-        if not t.is_contiguous():
-            raise ValueError("contiguous tensor expected")
-        out.append(t.data_ptr() or None)
-    return out
-
-
-def _on(stream):
-    """The raw handle of a stream, by default the current device's current one."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index == dev:
+        raw = stream.cuda_stream
+    else:
+        raise ValueError(f"stream of {stream.device}, the current device is cuda:{dev}")
+    return [t if t is None else t.data_ptr() or None for t in tensors] + [raw]
 
 
 def _router_for(router, logits):
@@ -629,8 +625,8 @@ def ep_route(router, logits, bias, topk_idx, topk_w, stream=None):
         _need(bias, torch.float32, (r.num_experts,), "bias")
     _need(topk_idx, torch.int64, (T, k), "topk_idx")
     _need(topk_w, torch.float32, (T, k), "topk_w")
-    ptrs = _here(logits, bias, topk_idx, topk_w)
-    _ok(load().ep_route(ctypes.byref(r), T, *ptrs, _on(stream)), "ep_route")
+    args = _here(stream, logits, bias, topk_idx, topk_w)
+    _ok(load().ep_route(ctypes.byref(r), T, *args), "ep_route")
 
 
 def ep_route_backward(router, logits, topk_idx, grad_topk_w, grad_logits, stream=None):
@@ -640,8 +636,8 @@ def ep_route_backward(router, logits, topk_idx, grad_topk_w, grad_logits, stream
     _need(topk_idx, torch.int64, (T, k), "topk_idx")
     _need(grad_topk_w, torch.float32, (T, k), "grad_topk_w")
     _need(grad_logits, logits.dtype, logits.shape, "grad_logits")
-    ptrs = _here(logits, topk_idx, grad_topk_w, grad_logits)
-    _ok(load().ep_route_backward(ctypes.byref(r), T, *ptrs, _on(stream)), "ep_route_backward")
+    args = _here(stream, logits, topk_idx, grad_topk_w, grad_logits)
+    _ok(load().ep_route_backward(ctypes.byref(r), T, *args), "ep_route_backward")
 
 
 def _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity) -> ep_expert_shape:
@@ -663,8 +659,8 @@ def ep_expert_gemm(expert_offset, a, a_scales, w, w_scales, out, num_ranks=1, ra
     N = w.shape[1]
     sh = _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity)
     _need(out, torch.bfloat16, (sh.rows, N), "out")
-    ptrs = _here(expert_offset, a, a_scales, w, w_scales, out)
-    _ok(load().ep_expert_gemm(ctypes.byref(sh), *ptrs, _on(stream)), "ep_expert_gemm")
+    args = _here(stream, expert_offset, a, a_scales, w, w_scales, out)
+    _ok(load().ep_expert_gemm(ctypes.byref(sh), *args), "ep_expert_gemm")
 
 
 def ep_expert_gated(expert_offset, a, a_scales, w, w_scales, out_q, out_scales, num_ranks=1, rank_capacity=0,
@@ -677,8 +673,8 @@ def ep_expert_gated(expert_offset, a, a_scales, w, w_scales, out_q, out_scales, 
     sh = _expert_shape(expert_offset, a, a_scales, w, w_scales, N, num_ranks, rank_capacity)
     _need(out_q, torch.uint8, (sh.rows, N), "out_q")
     _need(out_scales, torch.float32, (sh.rows, N // 128), "out_scales")
-    ptrs = _here(expert_offset, a, a_scales, w, w_scales, out_q, out_scales)
-    _ok(load().ep_expert_gated(ctypes.byref(sh), *ptrs, _on(stream)), "ep_expert_gated")
+    args = _here(stream, expert_offset, a, a_scales, w, w_scales, out_q, out_scales)
+    _ok(load().ep_expert_gated(ctypes.byref(sh), *args), "ep_expert_gated")
 
 
 def ep_combine_backward(shape, dy, expert_out, token_slot, topk_w, grad_expert_out, grad_topk_w, stream=None):
@@ -690,8 +686,8 @@ def ep_combine_backward(shape, dy, expert_out, token_slot, topk_w, grad_expert_o
     _need(topk_w, torch.float32, (T, k), "topk_w")
     _need(grad_expert_out, torch.bfloat16, (rows, H), "grad_expert_out")
     _need(grad_topk_w, torch.float32, (T, k), "grad_topk_w")
-    ptrs = _here(dy, expert_out, token_slot, topk_w, grad_expert_out, grad_topk_w)
-    _ok(load().ep_combine_backward(ctypes.byref(shape), *ptrs, _on(stream)), "ep_combine_backward")
+    args = _here(stream, dy, expert_out, token_slot, topk_w, grad_expert_out, grad_topk_w)
+    _ok(load().ep_combine_backward(ctypes.byref(shape), *args), "ep_combine_backward")
 
 
 def ep_accounting(shape, own_node, num_tokens_per_rank, num_tokens_per_node, rdma_algo_token_count,
