@@ -156,9 +156,9 @@ __device__ __forceinline__ void expert_rows(const int32_t *off, const ExpertShap
 }
 
 // Row tiles of BM rows are numbered without a pass over the experts first:
-// expert e's tiles are off[e] / BM + e and on.  As floor((o + n) / BM) + 1 >=
-// floor(o / BM) + ceil(n / BM), no two experts share a number, and rows / BM +
-// E numbers suffice; those without a tile end at once.  Every thread looks at
+// expert e's tiles are lo / BM + e and on, lo its first row.  As floor((o + n) /
+// BM) + 1 >= floor(o / BM) + ceil(n / BM), no two experts share a number, and
+// rows / BM + E numbers suffice; those without a tile end at once.  Every thread looks at
 // its share of the experts; the one that finds the tile names the expert.
 __device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape &s, int slot, int BM, int *found,
                                           int *expert, int *row, int *end) {
@@ -167,7 +167,7 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape 
     for (int e = threadIdx.x; e < s.E; e += blockDim.x) {
         int lo, hi;
         expert_rows(off, s, e, &lo, &hi);
-        const int first = max(off[e], 0) / BM + e;
+        const int first = lo / BM + e;
         if (slot >= first && slot - first < (hi - lo + BM - 1) / BM) *found = e;
     }
     __syncthreads();
@@ -175,7 +175,7 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape 
     if (e < 0) return false;
     int lo, hi;
     expert_rows(off, s, e, &lo, &hi);
-    const int r0 = lo + (slot - (max(off[e], 0) / BM + e)) * BM;
+    const int r0 = lo + (slot - (lo / BM + e)) * BM;
     *expert = e;
     *row = r0;
     *end = hi;

@@ -117,6 +117,15 @@ def test_rank_major_rows(ep, E, R, M, counts):
     _check_gated(ep, off, *_draw(rng, R * M, E, 256, 256), R, M)
 
 
+def test_rank_major_far_more_pairs_than_rows(ep):
+    """Blocks that drop most of their pairs: the segment starts lie far past the rows."""
+    rng = np.random.default_rng(17)
+    off = _offsets([70, 5, 0, 90, 300, 1, 20, 2, 0, 0, 50, 60, 8, 9, 10, 400])
+    R, M = 4, 40
+    _check_product(ep, off, *_draw(rng, R * M, 16, 256, 264), R, M)
+    _check_gated(ep, off, *_draw(rng, R * M, 16, 256, 256), R, M)
+
+
 def test_slice_of_the_offsets(ep):
     """One rank's experts: a slice of a dispatch's offsets with those experts' weights."""
     rng = np.random.default_rng(6)
