@@ -77,14 +77,17 @@ __global__ __launch_bounds__(kGradThreads) void ep_combine_backward_kernel(
                     for (int i = 0; i < kVecs; ++i) {
                         const int v = v0 + i * kGradThreads;
                         if (v >= nv) continue;
-                        vec16 g;
+                        float f[8];
+                        uint32_t g[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q) {
                             acc[j] = __builtin_fmaf(bf16_lo(x[i][q]), bf16_lo(o[j][i][q]), acc[j]);
                             acc[j] = __builtin_fmaf(bf16_hi(x[i][q]), bf16_hi(o[j][i][q]), acc[j]);
-                            g[q] = pack_bf16x2_cvt(w[j] * bf16_lo(x[i][q]), w[j] * bf16_hi(x[i][q]));
+                            f[2 * q] = w[j] * bf16_lo(x[i][q]);
+                            f[2 * q + 1] = w[j] * bf16_hi(x[i][q]);
                         }
-                        st16_nt(grad_out + s[j] * H + 8 * v, g);
+                        pack_bf16(f, g);
+                        st16_nt(grad_out + s[j] * H + 8 * v, vec16{g[0], g[1], g[2], g[3]});
                     }
                 }
             }

@@ -182,8 +182,30 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape 
     return r0 >= lo && r0 < hi;   // offsets that do not ascend: no tile
 }
 
-// h = g / (1 + e^-g) u
-__device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + expf(-g)) * u; }
+// h = g / (1 + e^-g) u.  The hardware's reciprocal is within one step, so h is
+// off by 3.5 steps at most: 1 of expf and of the reciprocal each, half of the
+// sum and of the two products each.
+__device__ __forceinline__ float gate(float g, float u) { return g * __builtin_amdgcn_rcpf(1.0f + expf(-g)) * u; }
+
+// Four values over a scale >= their largest magnitude / 448, as e4m3 bytes.  The
+// quotients are those of the IEEE division (a correctly rounded reciprocal and
+// one correction of the quotient by its remainder; at the ends of the range the
+// division itself), a third of its instructions; they stay below 464, from
+// where the conversion would not round to 448.
+struct Divisor {
+    float scale, inv;
+    bool plain;
+    __device__ __forceinline__ explicit Divisor(float s) : scale(s), inv(1.0f / s), plain(s > 0x1p-100f && s < 0x1p100f) {}
+    __device__ __forceinline__ float over(float h) const {
+        if (!plain) return h / scale;
+        const float q = h * inv;
+        return __builtin_fmaf(__builtin_fmaf(-q, scale, h), inv, q);
+    }
+    __device__ __forceinline__ uint32_t quantise(float a, float b, float c, float d) const {
+        int v = __builtin_amdgcn_cvt_pk_fp8_f32(over(a), over(b), 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(over(c), over(d), v, true);
+    }
+};
 
 // ---------------------------------------------------------------- few rows
 
@@ -371,14 +393,16 @@ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             const int r = row + 16 * m + r16;
+            float v[8];
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = acc[i / 4][m][i % 4];
+            pack_bf16(v, o);
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
                 const int n = n0 + 16 * f + 4 * quad;   // N % 8 == 0: all 4 in or all out
                 if (r >= end || n >= s.N) continue;
-                uint2 v;
-                v.x = pack_bf16x2(acc[f][m][0], acc[f][m][1]);
-                v.y = pack_bf16x2(acc[f][m][2], acc[f][m][3]);
-                *reinterpret_cast<uint2 *>(out + (size_t)r * s.N + n) = v;
+                *reinterpret_cast<uint2 *>(out + (size_t)r * s.N + n) = uint2{o[2 * f], o[2 * f + 1]};
             }
         }
     } else {
@@ -410,11 +434,9 @@ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
 #pragma unroll
             for (int c = 0; c < kColWaves; ++c) top = fmaxf(top, amax[c][16 * m + r16]);
             const float scale = (top == 0.0f) ? 1.0f : top / 448.0f;
-            uint32_t q = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q |= f32_to_e4m3(h[m][i] / scale) << (8 * i);
             if (r >= end) continue;
-            *reinterpret_cast<uint32_t *>(oq + (size_t)r * s.N + n0 + 4 * quad) = q;
+            *reinterpret_cast<uint32_t *>(oq + (size_t)r * s.N + n0 + 4 * quad) =
+                Divisor(scale).quantise(h[m][0], h[m][1], h[m][2], h[m][3]);
             if (col == 0 && quad == 0) oqs[(size_t)r * (s.N / 128) + ct] = scale;
         }
     }
@@ -424,30 +446,23 @@ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
 
 constexpr int kTileThreads = 512, kTileN = 256;   // 8 waves; weight rows of a tile
 
-// One block: BM rows by 256 weight rows (gated: 128 gate rows and the matching
-// 128 up rows), 8 waves, 2 by 4.  Both operands of a block of K = 128 are
+// One block: BM rows by 256 weight rows, 8 waves, 2 by 4.  Both operands of a block of K = 128 are
 // staged in LDS, 2 or 3 buffers in turn: the next blocks' loads are in flight
 // while this one is multiplied.
-template <int BM, bool GATED>
+template <int BM>
 __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
-    uint16_t *out, uint8_t *oq, float *oqs, int slots, int cols) {
+    uint16_t *out, int slots, int cols) {
     constexpr int WN = 2, WM = 4, NF = kTileN / WN / 16, MF = BM / WM / 16;
     constexpr int STAGES = BM <= 128 ? 3 : 2;      // what fits 160 KiB of LDS
-    constexpr int HALF = GATED ? 2 : 1;            // gate and up, or one product
-    constexpr int WCOLS = kTileN / HALF / WN;      // columns of the result per wave
-    typedef Operand<GATED> Op;
     __shared__ __attribute__((aligned(16))) uint8_t buf0[(kTileN + BM) * 128];
     __shared__ __attribute__((aligned(16))) uint8_t buf1[(kTileN + BM) * 128];
     __shared__ __attribute__((aligned(16))) uint8_t buf2[STAGES == 3 ? (kTileN + BM) * 128 : 16];
     __shared__ int found;
-    __shared__ float amax[GATED ? WN : 1][GATED ? BM : 1];
 
-    // consecutive blocks go to the 8 XCDs in turn; each XCD takes a contiguous
-    // eighth of the tiles, 8 row tiles by all columns at a time, so that the
-    // 32 blocks it runs together share their operands in its L2
-    const int tile = (int)blockIdx.x;
-    const int per = 8 * cols, sb = tile / per, in = tile % per;
+    // 8 row tiles by all columns at a time, a row tile's columns on one XCD
+    // (689 us; an eighth of the tiles to each XCD as the gated tiles have it 760)
+    const int per = 8 * cols, sb = blockIdx.x / per, in = blockIdx.x % per;
     const int slot = sb * 8 + in % 8, ct = in / 8;
     if (slot >= slots) return;
     int e, row, end;
@@ -457,102 +472,88 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     const int wn = wid % WN, wm = wid / WN;
     const int r16 = lane & 15, quad = lane >> 4;
     const int KB = s.K / 128;
-    const int wrows = HALF * s.N;
-    const int n0 = ct * (kTileN / HALF);           // first column of the result
-    const uint8_t *we = w + (size_t)e * wrows * s.K;
-    const float *wse = ws + (size_t)e * ((wrows + 127) / 128) * KB;
+    const int n0 = ct * kTileN;                    // first column of the result
+    const uint8_t *w0 = w + ((size_t)e * s.N + n0) * s.K;
+    const float *wse = ws + (size_t)e * ((s.N + 127) / 128) * KB;
 
     // staging: pass p of the block covers 64 rows, a wave 8 of them
     const int srow = wid * 8 + (lane >> 3);                    // + 64 p
     const uint32_t piece = (uint32_t)(((lane & 7) ^ (srow & 7)) << 4);
-    // gated: all 128 rows of gate and of up are there, 64 rows on is a scalar
-    // offset; else the last tile's rows past the end repeat the last one
-    uint32_t woff[GATED ? 1 : kTileN / 64], xoff[BM / 64];
+    // rows past the last repeat it
+    uint32_t woff[kTileN / 64], xoff[BM / 64];
 #pragma unroll
-    for (int p = 0; p < (GATED ? 1 : kTileN / 64); ++p)
-        woff[p] = (uint32_t)(GATED ? srow : min(srow + 64 * p, wrows - 1 - n0)) * (uint32_t)s.K + piece;
+    for (int p = 0; p < kTileN / 64; ++p)
+        woff[p] = (uint32_t)min(srow + 64 * p, s.N - 1 - n0) * (uint32_t)s.K + piece;
 #pragma unroll
     for (int p = 0; p < BM / 64; ++p)
         xoff[p] = (uint32_t)min(srow + 64 * p, end - 1 - row) * (uint32_t)s.K + piece;
-    const uint8_t *w0 = we + (size_t)n0 * s.K;
-    const rsrc_t wb0 = buffer(w0), wb1 = buffer(GATED ? w0 + (size_t)s.N * s.K : w0);
-    const rsrc_t xb = buffer(a + (size_t)row * s.K);
+    const rsrc_t wb = buffer(w0), xb = buffer(a + (size_t)row * s.K);
 
     constexpr int PIECES = (kTileN + BM) / 64;
     static_assert(PIECES <= 15, "the waits' counts");
     const auto stage = [&](uint8_t *buf, int kb, int p) {   // piece p of a block of K
         const uint32_t past = kb < KB ? 0u : 0x80000000u;
-        if (GATED && p < kTileN / 64)
-            load_to_lds(p < 2 ? wb0 : wb1, buf + p * 8192 + wid * 1024, woff[0] | past, (p & 1) * 64 * s.K + kb * 128);
-        else if (p < kTileN / 64)
-            load_to_lds(wb0, buf + p * 8192 + wid * 1024, woff[p] | past, kb * 128);
+        if (p < kTileN / 64)
+            load_to_lds(wb, buf + p * 8192 + wid * 1024, woff[p] | past, kb * 128);
         else
             load_to_lds(xb, buf + p * 8192 + wid * 1024, xoff[p - kTileN / 64] | past, kb * 128);
     };
 
-    // scales: one register per lane and group of 16 rows, one (or gate's and
-    // up's) per wave, loaded a block ahead
+    // scales: one register per lane and group of 16 rows, one per wave (its 128
+    // weight rows are one block of theirs), loaded a block ahead
     const rsrc_t asb = buffer(as + (size_t)row * KB), wsb = buffer(wse);
-    uint32_t asoff[MF], wsoff[HALF];
+    uint32_t asoff[MF];
 #pragma unroll
     for (int m = 0; m < MF; ++m)
         asoff[m] = (uint32_t)min(wm * 16 * MF + 16 * m + r16, end - 1 - row) * (uint32_t)KB * 4;
-#pragma unroll
-    for (int h = 0; h < HALF; ++h)
-        wsoff[h] = (uint32_t)(min(n0 + h * s.N + wn * WCOLS, wrows - 1) / 128) * (uint32_t)KB * 4;
+    const uint32_t wsoff = (uint32_t)(min(n0 + wn * 128, s.N - 1) / 128) * (uint32_t)KB * 4;
 
     f32x4 acc[NF][MF] = {};
-    float sx[MF], sw[HALF];
+    float sx[MF], sw;
     const auto scales = [&](int kb) {
 #pragma unroll
         for (int m = 0; m < MF; ++m) sx[m] = load_f32(asb, asoff[m], kb * 4);
-#pragma unroll
-        for (int h = 0; h < HALF; ++h) sw[h] = load_f32(wsb, wsoff[h], kb * 4);
+        sw = load_f32(wsb, wsoff, kb * 4);
     };
     const uint32_t plo = (uint32_t)((quad ^ (r16 & 7)) << 4), phi = plo ^ 64;
-    const uint32_t wlo = (uint32_t)(wn * WCOLS + r16) * 128 + plo, whi = (uint32_t)(wn * WCOLS + r16) * 128 + phi;
+    const uint32_t wlo = (uint32_t)(wn * 128 + r16) * 128 + plo, whi = wlo ^ 64;
     const uint32_t xrow = (uint32_t)(kTileN + wm * 16 * MF + r16) * 128;
     const uint32_t xlo = xrow + plo, xhi = xrow + phi;
-    const auto multiply = [&](const uint8_t *buf, const float (&x)[MF], const float (&c)[HALF], const auto &between) {
-        typename Op::type xf[MF];
+    const auto multiply = [&](const uint8_t *buf, const float (&x)[MF], float c, const auto &between) {
+        i32x8 xf[MF];
 #pragma unroll
-        for (int m = 0; m < MF; ++m) xf[m] = Op::make(lds_operand(buf + xlo + 2048 * m, buf + xhi + 2048 * m));
-        const auto weights = [&](int n) {
-            const int at = GATED ? n / (NF / 2) * 128 * 128 + 2048 * (n % (NF / 2)) : 2048 * n;
-            return lds_operand(buf + wlo + at, buf + whi + at);
-        };
+        for (int m = 0; m < MF; ++m) xf[m] = lds_operand(buf + xlo + 2048 * m, buf + xhi + 2048 * m);
+        const auto weights = [&](int n) { return lds_operand(buf + wlo + 2048 * n, buf + whi + 2048 * n); };
         const auto add = [&](int n, const f32x4 (&d)[MF]) {
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
-                const float sc = x[m] * c[GATED ? n / (NF / 2) : 0];
+                const float sc = x[m] * c;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[n][m][i] = __builtin_fmaf(d[m][i], sc, acc[n][m][i]);
                 asm volatile("" : "+v"(acc[n][m]));   // added here, not sunk into the next block of K
             }
         };
-        // While the products with weights n run, the next weights are widened,
-        // those after next are on their way and the last products are scaled.
-        // The fences keep the scheduler from fetching everything at once.
-        auto wf = Op::make(weights(0));
-        i32x8 wraw = weights(1);
+        // While the products with weights n run, those after next are on their
+        // way and the last products are scaled.  The fences keep the scheduler
+        // from fetching everything at once.
+        i32x8 wf[2] = {weights(0), weights(1)};
         f32x4 last[MF];
 #pragma unroll
         for (int n = 0; n < NF; ++n) {
             const i32x8 wnext = weights(n + 2 < NF ? n + 2 : NF - 1);
-            const auto wf1 = Op::make(wraw);
             f32x4 d[MF];
-            Op::multiply(wf, xf, d);
+            Operand<false>::multiply(wf[0], xf, d);
             if (n > 0) add(n - 1, last);
             between(n);
             __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // 2 reads of LDS, then in turn
 #pragma unroll
-            for (int m = 0; m < (GATED ? 4 : 1) * MF; ++m) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // a matrix instruction
-                __builtin_amdgcn_sched_group_barrier(0x002, GATED ? 2 : 4, 0);  // and vector ones
+            for (int m = 0; m < MF; ++m) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
+                __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // and 4 vector ones
             }
             __builtin_amdgcn_sched_barrier(0);
-            wf = wf1;
-            wraw = wnext;
+            wf[0] = wf[1];
+            wf[1] = wnext;
 #pragma unroll
             for (int m = 0; m < MF; ++m) last[m] = d[m];
         }
@@ -568,11 +569,10 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
         // and the buffer of the block before is free
         __builtin_amdgcn_s_waitcnt(0x0F70 | (STAGES - 2) * PIECES);
         barrier_only();
-        float x[MF], c[HALF];
+        float x[MF];
+        const float c = sw;
 #pragma unroll
         for (int m = 0; m < MF; ++m) x[m] = sx[m];
-#pragma unroll
-        for (int h = 0; h < HALF; ++h) c[h] = sw[h];
         scales(min(kb + 1, KB - 1));
         __builtin_amdgcn_sched_barrier(0);
         multiply(cur, x, c, [&](int n) {
@@ -593,54 +593,224 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);
 
-    if constexpr (!GATED) {
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int r = row + wm * 16 * MF + 16 * m + r16;
+    for (int m = 0; m < MF; ++m) {
+        const int r = row + wm * 16 * MF + 16 * m + r16;
+        float v[4 * NF];
+        uint32_t o[2 * NF];
 #pragma unroll
-            for (int n = 0; n < NF; ++n) {
-                const int c = n0 + wn * WCOLS + 16 * n + 4 * quad;   // N % 8 == 0: all 4 in or all out
-                if (r >= end || c >= s.N) continue;
-                uint2 v;
-                v.x = pack_bf16x2(acc[n][m][0], acc[n][m][1]);
-                v.y = pack_bf16x2(acc[n][m][2], acc[n][m][3]);
-                *reinterpret_cast<uint2 *>(out + (size_t)r * s.N + c) = v;
-            }
+        for (int i = 0; i < 4 * NF; ++i) v[i] = acc[i / 4][m][i % 4];
+        pack_bf16(v, o);
+#pragma unroll
+        for (int n = 0; n < NF; ++n) {
+            const int c = n0 + wn * 128 + 16 * n + 4 * quad;   // N % 8 == 0: all 4 in or all out
+            if (r < end && c < s.N) *reinterpret_cast<uint2 *>(out + (size_t)r * s.N + c) = uint2{o[2 * n], o[2 * n + 1]};
         }
-    } else {
-        // h takes the place of the gate's accumulators
+    }
+}
+
+// ---------------------------------------------------------------- many rows, 16-bit products
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// 16 bytes of e4m3 as two operands of the 32 x 32 x 16 instruction.
+struct Pair {
+    f16x8 v[2];
+};
+__device__ __forceinline__ Pair widen16(vec16 b) {
+    Pair w;
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            float top = 0.0f;
+    for (int i = 0; i < 4; ++i) {
+        const f16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b[i], 1.0f, false);
+        const f16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)b[i], 1.0f, true);
+        w.v[i / 2][4 * (i % 2) + 0] = lo[0];
+        w.v[i / 2][4 * (i % 2) + 1] = lo[1];
+        w.v[i / 2][4 * (i % 2) + 2] = hi[0];
+        w.v[i / 2][4 * (i % 2) + 3] = hi[1];
+    }
+    return w;
+}
+
+// The gated product in tiles of 128 rows by 128 gate and the matching 128 up
+// rows: 8 waves, 4 by 2, each 32 gate and 32 up rows by 64 rows of a.  The
+// widening and the scaling take 3 vector instructions for every 16 cycles of
+// matrix instructions; beside 16 x 16 x 32 ones two of those are free, beside
+// 32 x 32 x 16 ones, half as many to issue, three (measured: 19.5 against 24
+// cycles).  Three buffers of LDS: two blocks of K are under way.
+__global__ __launch_bounds__(kTileThreads) void ep_expert_gated_tile_kernel(
+    ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
+    uint8_t *oq, float *oqs, int slots, int cols) {
+    constexpr int BM = 128, WN = 4, PIECES = (kTileN + BM) / 64, BYTES = (kTileN + BM) * 128;
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[BYTES];
+    __shared__ int found;
+    __shared__ float amax[WN][BM];
+
+    // consecutive blocks go to the 8 XCDs in turn; each XCD takes an eighth of
+    // the tiles, 8 row tiles by 4 columns together, which share their operands
+    // in its L2 (1929 us against 2043 with all columns of 2 row tiles together)
+    const int tile = (int)(blockIdx.x % 8) * (int)(gridDim.x / 8) + (int)(blockIdx.x / 8);
+    const int per = 8 * cols, in = tile % per, group = in / 32, wide = min(4, cols - 4 * group);
+    const int slot = tile / per * 8 + (in - 32 * group) / wide, ct = 4 * group + (in - 32 * group) % wide;
+    if (slot >= slots) return;
+    int e, row, end;
+    if (!find_tile(off, s, slot, BM, &found, &e, &row, &end)) return;
+
+    const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wn = wid % WN, wm = wid / WN;
+    const int r32 = lane & 31, half = lane >> 5;
+    const int KB = s.K / 128;
+    const uint8_t *we = w + ((size_t)e * 2 * s.N + (size_t)ct * 128) * s.K;   // N % 128 == 0: all 128 rows are there
+    const float *wse = ws + (size_t)e * (2 * s.N / 128) * KB;
+
+    const int srow = wid * 8 + (lane >> 3);                    // + 64 p
+    const uint32_t piece = (uint32_t)(((lane & 7) ^ (srow & 7)) << 4);
+    const uint32_t woff = (uint32_t)srow * (uint32_t)s.K + piece;
+    uint32_t xoff[BM / 64];
 #pragma unroll
-            for (int n = 0; n < NF / 2; ++n)
+    for (int p = 0; p < BM / 64; ++p)
+        xoff[p] = (uint32_t)min(srow + 64 * p, end - 1 - row) * (uint32_t)s.K + piece;
+    const rsrc_t wb0 = buffer(we), wb1 = buffer(we + (size_t)s.N * s.K), xb = buffer(a + (size_t)row * s.K);
+    const auto stage = [&](uint8_t *buf, int kb, int p) {   // piece p of a block of K
+        const uint32_t past = kb < KB ? 0u : 0x80000000u;
+        if (p < kTileN / 64)
+            load_to_lds(p < 2 ? wb0 : wb1, buf + p * 8192 + wid * 1024, woff | past, (p & 1) * 64 * s.K + kb * 128);
+        else
+            load_to_lds(xb, buf + p * 8192 + wid * 1024, xoff[p - kTileN / 64] | past, kb * 128);
+    };
+
+    const rsrc_t asb = buffer(as + (size_t)row * KB), wsb = buffer(wse);
+    uint32_t asoff[2], wsoff[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[n][m][i] = gate(acc[n][m][i], acc[n + NF / 2][m][i]);
-                    top = fmaxf(top, fabsf(acc[n][m][i]));
+    for (int m = 0; m < 2; ++m) asoff[m] = (uint32_t)min(wm * 64 + 32 * m + r32, end - 1 - row) * (uint32_t)KB * 4;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) wsoff[f] = (uint32_t)(ct + f * (s.N / 128)) * (uint32_t)KB * 4;
+    float sx[2], sw[2];
+    const auto scales = [&](int kb) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) sx[m] = load_f32(asb, asoff[m], kb * 4);
+#pragma unroll
+        for (int f = 0; f < 2; ++f) sw[f] = load_f32(wsb, wsoff[f], kb * 4);
+    };
+
+    // a lane's 16 bytes of quarter q of a row: piece 2 q + half, permuted by the row
+    const uint32_t wrow = (uint32_t)(wn * 32 + r32) * 128, xrow = (uint32_t)(kTileN + wm * 64 + r32) * 128;
+    const uint32_t p0 = (uint32_t)((half ^ (r32 & 7)) << 4);
+    vec16 raw[4];      // gate, up, two groups of rows of a: the quarter after the next
+    Pair o[4];         // the next quarter, widened
+    const auto read = [&](const uint8_t *buf, int q) {
+        const uint32_t p = p0 ^ (uint32_t)(q << 5);
+        raw[0] = ld16(buf + wrow + p);
+        raw[1] = ld16(buf + wrow + p + 128 * 128);
+        raw[2] = ld16(buf + xrow + p);
+        raw[3] = ld16(buf + xrow + p + 32 * 128);
+    };
+    f32x16 acc[2][2] = {}, d[2][2] = {};
+    float x[2] = {}, c[2] = {};
+    const auto add = [&](int t) {   // the sums of the last block, scaled
+        const float sc = x[t >> 1] * c[t & 1];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            acc[t & 1][t >> 1][i] = __builtin_fmaf(d[t & 1][t >> 1][i], sc, acc[t & 1][t >> 1][i]);
+        asm volatile("" : "+v"(acc[t & 1][t >> 1]));   // added here, not later
+    };
+    // The quarters of all blocks form one chain: while one is multiplied, the
+    // next is widened and the one after that read from LDS, across the change
+    // of the block too, so that nothing waits for LDS behind a barrier.
+    const auto step = [&](const uint8_t *cur, const uint8_t *after, uint8_t *next, int kb) {
+        float nx[2], nc[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) nx[m] = sx[m], nc[m] = sw[m];
+        scales(min(kb + 1, KB - 1));
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q == 2) {
+                // from here on the next block is read: it has arrived in every
+                // wave (of later loads, the 4 pieces staged above may be under
+                // way), and every wave has read the last of this one, whose
+                // buffer is filled again from the next step on
+                __builtin_amdgcn_s_waitcnt(0x0074);   // lgkmcnt(0), vmcnt(4)
+                barrier_only();
+            }
+            Pair n[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) n[i] = widen16(raw[i]);
+            read(q < 2 ? cur : after, (q + 2) % 4);
+            if (q < 3)
+#pragma unroll
+                for (int p = q * 2; p < q * 2 + 2; ++p) stage(next, kb + 2, p);
+            const f32x16 zero = {};
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    if (q + k == 0) add(t);
+                    d[t & 1][t >> 1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(o[t & 1].v[k], o[2 + (t >> 1)].v[k],
+                                                                              q + k ? d[t & 1][t >> 1] : zero, 0, 0, 0);
                 }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (quad == 0) amax[wn][wm * 16 * MF + 16 * m + r16] = top;
-        }
-        __syncthreads();
+            if (q > 0) {
 #pragma unroll
-        for (int m = 0; m < MF; ++m) {
-            const int i = wm * 16 * MF + 16 * m + r16, r = row + i;
-            float top = 0.0f;
-#pragma unroll
-            for (int c = 0; c < WN; ++c) top = fmaxf(top, amax[c][i]);
-            const float scale = (top == 0.0f) ? 1.0f : top / 448.0f;
-            if (r >= end) continue;
-#pragma unroll
-            for (int n = 0; n < NF / 2; ++n) {
-                uint32_t q = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q |= f32_to_e4m3(acc[n][m][j] / scale) << (8 * j);
-                *reinterpret_cast<uint32_t *>(oq + (size_t)r * s.N + n0 + wn * WCOLS + 16 * n + 4 * quad) = q;
+                for (int t = 0; t < 8; ++t) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // a matrix instruction
+                    __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);   // and 4 vector ones
+                }
             }
-            if (wn == 0 && quad == 0) oqs[(size_t)r * (s.N / 128) + ct] = scale;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = n[i];
         }
+#pragma unroll
+        for (int m = 0; m < 2; ++m) x[m] = nx[m], c[m] = nc[m];
+    };
+    static_assert(PIECES == 6, "two pieces in each of the first three quarters");
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) stage(buf0, 0, p);
+    scales(0);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) stage(buf1, 1, p);
+    __builtin_amdgcn_s_waitcnt(0x0F70 | PIECES);
+    barrier_only();
+    read(buf0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = widen16(raw[i]);
+    read(buf0, 1);
+    for (int kb = 0; kb < KB; kb += 3) {
+        step(buf0, buf1, buf2, kb);
+        if (kb + 1 < KB) step(buf1, buf2, buf0, kb + 1);
+        if (kb + 2 < KB) step(buf2, buf0, buf1, kb + 2);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) add(t);
+
+    // value i of a lane: column 8 (i / 4) + 4 half + i % 4, row r32 of each group
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            acc[0][m][i] = gate(acc[0][m][i], acc[1][m][i]);
+            top = fmaxf(top, fabsf(acc[0][m][i]));
+        }
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (half == 0) amax[wn][wm * 64 + 32 * m + r32] = top;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const int i = wm * 64 + 32 * m + r32, r = row + i;
+        const float top = fmaxf(fmaxf(amax[0][i], amax[1][i]), fmaxf(amax[2][i], amax[3][i]));
+        const float scale = (top == 0.0f) ? 1.0f : top / 448.0f;
+        if (r >= end) continue;
+        uint8_t *o = oq + (size_t)r * s.N + ct * 128 + wn * 32 + 4 * half;
+        const Divisor by(scale);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<uint32_t *>(o + 8 * g) = by.quantise(acc[0][m][4 * g], acc[0][m][4 * g + 1],
+                                                                   acc[0][m][4 * g + 2], acc[0][m][4 * g + 3]);
+        if (wn == 0 && half == 0) oqs[(size_t)r * (s.N / 128) + ct] = scale;
     }
 }
 
@@ -655,13 +825,22 @@ bool expert_grid_fits(const ExpertShape &s, bool gated) {
 
 namespace {
 
-template <int BM, bool GATED>
+template <int BM>
 hipError_t launch_tile(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
-                       const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
-    const int slots = (int)tile_slots(s, BM), cols = GATED ? s.N / 128 : (s.N + kTileN - 1) / kTileN;
+                       const uint8_t *w, const float *ws, uint16_t *out, hipStream_t stream) {
+    const int slots = (int)tile_slots(s, BM), cols = (s.N + kTileN - 1) / kTileN;
     const int64_t blocks = (int64_t)((slots + 7) / 8) * 8 * cols;
-    hipLaunchKernelGGL((ep_expert_tile_kernel<BM, GATED>), dim3((unsigned)blocks), dim3(kTileThreads), 0, stream,
-                       s, offset, a, as, w, ws, out, q, qs, slots, cols);
+    hipLaunchKernelGGL(ep_expert_tile_kernel<BM>, dim3((unsigned)blocks), dim3(kTileThreads), 0, stream, s, offset, a,
+                       as, w, ws, out, slots, cols);
+    return hipGetLastError();
+}
+
+hipError_t launch_gated_tile(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
+                             const uint8_t *w, const float *ws, uint8_t *q, float *qs, hipStream_t stream) {
+    const int slots = (int)tile_slots(s, 128), cols = s.N / 128;
+    const int64_t blocks = (int64_t)((slots + 7) / 8) * 8 * cols;
+    hipLaunchKernelGGL(ep_expert_gated_tile_kernel, dim3((unsigned)blocks), dim3(kTileThreads), 0, stream, s, offset,
+                       a, as, w, ws, q, qs, slots, cols);
     return hipGetLastError();
 }
 
@@ -694,12 +873,12 @@ hipError_t launch_product(const ExpertShape &s, const int32_t *offset, const uin
     const auto tiles = [&](int BM) { return (s.rows / BM + 1) * cols; };
     if constexpr (GATED) {
         if (mean >= 160 && tiles(192) >= 192)
-            return launch_tile<192, true>(s, offset, a, as, w, ws, out, q, qs, stream);
+            return launch_gated_tile(s, offset, a, as, w, ws, q, qs, stream);
     } else {
         if (mean >= 96 && tiles(256) >= 192)
-            return launch_tile<256, false>(s, offset, a, as, w, ws, out, q, qs, stream);
+            return launch_tile<256>(s, offset, a, as, w, ws, out, stream);
         if (mean >= 40 && tiles(128) >= 192)
-            return launch_tile<128, false>(s, offset, a, as, w, ws, out, q, qs, stream);
+            return launch_tile<128>(s, offset, a, as, w, ws, out, stream);
     }
     if (mean < 16 && (s.rows < s.E ? s.rows : s.E) * cols < 512)
         return launch_stream<1, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
