@@ -143,16 +143,15 @@ __device__ __forceinline__ i32x8 lds_operand(const uint8_t *lo16, const uint8_t 
 // The rows of expert e in a and the output, clamped into [0, rows].
 __device__ __forceinline__ void expert_rows(const int32_t *off, const ExpertShape &s, int e, int *lo, int *hi) {
     const int rows = (int)s.rows;
-    int b = off[e], t = off[e + 1];
+    int64_t b = off[e], t = off[e + 1];
     if (s.M > 0) {
         const int r = e / (s.E / s.R), first = off[r * (s.E / s.R)];
-        const int end = (r + 1) * s.M;
-        b = min(b - first + r * s.M, end);
-        t = min(t - first + r * s.M, end);
+        const int64_t shift = (int64_t)r * s.M - first, end = (int64_t)(r + 1) * s.M;
+        b = min(b + shift, end);
+        t = min(t + shift, end);
     }
-    b = min(max(b, 0), rows);
-    *lo = b;
-    *hi = min(max(t, b), rows);
+    *lo = (int)min(max(b, (int64_t)0), (int64_t)rows);
+    *hi = (int)min(max(t, (int64_t)*lo), (int64_t)rows);
 }
 
 // Row tiles of BM rows are numbered without a pass over the experts first:
@@ -209,11 +208,10 @@ struct Divisor {
 
 // ---------------------------------------------------------------- few rows
 
-constexpr int kColWaves = 8;   // waves side by side: 16 weight rows twice each
-
-// BM = 16 MT rows by 256 weight rows (gated: 128 columns of gate and the same
-// 128 of up, one scale group of the result), K split over KS groups of 8 waves
-// whose parts are added in LDS in their order.  Here the weights are what
+// BM = 16 MT rows by 32 CW weight rows (gated: CW = 8, 128 columns of gate and
+// the same 128 of up, one scale group of the result), CW waves side by side
+// with 16 weight rows twice each, K split over KS groups of them whose parts
+// are added in LDS in their order.  Here the weights are what
 // counts: each is read once.  Loading them straight into the operands' layout
 // costs the address unit a cycle per lane pair, as neighbouring lanes hold
 // different rows, and bounds the kernel at a third of the memory rate; so each
@@ -221,15 +219,17 @@ constexpr int kColWaves = 8;   // waves side by side: 16 weight rows twice each
 // lines) into its own part of LDS and reads the operands from there, with two
 // blocks in flight and no barrier.  The rows of a are shared by the waves: XB
 // blocks of K at a time, two buffers, a barrier per change.
-template <int MT, int KS, bool GATED>
+template <int MT, int CW, int KS, bool GATED>
 __global__ __attribute__((amdgpu_waves_per_eu(4, 4)))
-__launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
+__launch_bounds__(64 * CW * KS) void ep_expert_stream_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
     uint16_t *out, uint8_t *oq, float *oqs, int cols) {
-    constexpr int XB = 2;                        // blocks of K of a's rows per change
-    constexpr int XBYTES = 16 * MT * 128 * XB;   // 4 or 8 KiB
-    __shared__ __attribute__((aligned(16))) uint8_t wbuf0[kColWaves * KS * 4096];
-    __shared__ __attribute__((aligned(16))) uint8_t wbuf1[kColWaves * KS * 4096];
+    constexpr int XB = KS > 2 ? 1 : 2;           // blocks of K of a's rows per change
+    constexpr int XBYTES = 16 * MT * 128 * XB;   // 2, 4 or 8 KiB
+    static_assert(!GATED || CW == 8, "a scale group of the result per block");
+    static_assert(XBYTES <= 1024 * CW, "one piece of a's rows per wave");
+    __shared__ __attribute__((aligned(16))) uint8_t wbuf0[CW * KS * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t wbuf1[CW * KS * 4096];
     __shared__ __attribute__((aligned(16))) uint8_t xbuf0[KS * XBYTES];
     __shared__ __attribute__((aligned(16))) uint8_t xbuf1[KS * XBYTES];
     // two blocks share a CU's 160 KiB to the byte: the tile's expert and the
@@ -245,12 +245,12 @@ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
     __syncthreads();   // everyone has read it
 
     const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int col = wid % kColWaves, ks = wid / kColWaves;
+    const int col = wid % CW, ks = wid / CW;
     const int r16 = lane & 15, quad = lane >> 4;
     const int KB = s.K / 128;
     const int wrows = GATED ? 2 * s.N : s.N;
     // the two groups of 16 weight rows of this wave
-    const int n0 = GATED ? ct * 128 + col * 16 : ct * 256 + col * 32;
+    const int n0 = GATED ? ct * 128 + col * 16 : (ct * CW + col) * 32;
     const int n1 = GATED ? n0 + s.N : n0 + 16;
     const uint8_t *we = w + (size_t)e * wrows * s.K;
     const float *wse = ws + (size_t)e * ((wrows + 127) / 128) * KB;
@@ -378,14 +378,14 @@ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
         if (ks > 0)
 #pragma unroll
             for (int m = 0; m < 2 * MT; ++m)
-                part[(((ks - 1) * kColWaves + col) * 2 * MT + m) * kWave + lane] = acc[m & 1][m >> 1];
+                part[(((ks - 1) * CW + col) * 2 * MT + m) * kWave + lane] = acc[m & 1][m >> 1];
         __syncthreads();
         if (ks == 0)
 #pragma unroll
             for (int p = 0; p < KS - 1; ++p)
 #pragma unroll
                 for (int m = 0; m < 2 * MT; ++m)
-                    acc[m & 1][m >> 1] += part[((p * kColWaves + col) * 2 * MT + m) * kWave + lane];
+                    acc[m & 1][m >> 1] += part[((p * CW + col) * 2 * MT + m) * kWave + lane];
     }
 
     if constexpr (!GATED) {
@@ -432,7 +432,7 @@ __launch_bounds__(64 * kColWaves * KS) void ep_expert_stream_kernel(
             const int r = row + 16 * m + r16;
             float top = 0.0f;
 #pragma unroll
-            for (int c = 0; c < kColWaves; ++c) top = fmaxf(top, amax[c][16 * m + r16]);
+            for (int c = 0; c < CW; ++c) top = fmaxf(top, amax[c][16 * m + r16]);
             const float scale = (top == 0.0f) ? 1.0f : top / 448.0f;
             if (r >= end) continue;
             *reinterpret_cast<uint32_t *>(oq + (size_t)r * s.N + n0 + 4 * quad) =
@@ -818,9 +818,11 @@ int64_t tile_slots(const ExpertShape &s, int BM) { return s.rows / BM + s.E; }
 
 }  // namespace
 
+// The widest grid is that of the 32-row form (the ones with narrower blocks are
+// taken for a few hundred of them only).
 bool expert_grid_fits(const ExpertShape &s, bool gated) {
     const int64_t cols = gated ? s.N / 128 : (s.N + 255) / 256;
-    return tile_slots(s, 16) * cols * 1024 < (int64_t(1) << 32);
+    return (tile_slots(s, 32) + 8) * cols * kTileThreads < (int64_t(1) << 32);
 }
 
 namespace {
@@ -844,45 +846,51 @@ hipError_t launch_gated_tile(const ExpertShape &s, const int32_t *offset, const 
     return hipGetLastError();
 }
 
-template <int MT, int KS, bool GATED>
+template <int MT, int CW, int KS, bool GATED>
 hipError_t launch_stream(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                          const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
-    const int cols = GATED ? s.N / 128 : (s.N + 255) / 256;
-    hipLaunchKernelGGL((ep_expert_stream_kernel<MT, KS, GATED>), dim3((unsigned)(tile_slots(s, 16 * MT) * cols)),
-                       dim3(kWave * kColWaves * KS), 0, stream, s, offset, a, as, w, ws, out, q, qs, cols);
+    const int cols = GATED ? s.N / 128 : (s.N + 32 * CW - 1) / (32 * CW);
+    hipLaunchKernelGGL((ep_expert_stream_kernel<MT, CW, KS, GATED>), dim3((unsigned)(tile_slots(s, 16 * MT) * cols)),
+                       dim3(kWave * CW * KS), 0, stream, s, offset, a, as, w, ws, out, q, qs, cols);
     return hipGetLastError();
 }
 
 // Which form: by the rows of an expert on average, all that the host knows of
-// them, and by whether the tiles fill the 256 CUs.  Measured on uniform routing
-// over 32 experts, K = 7168 and 4096 (gated) or 2048 weight rows, and over 96
-// experts, K = 1024 and 768 or 384 weight rows (us):
-//   mean rows           8 (32)  32 (32)  128 (32)  256 (32)  1024 (32)  171 (96)
-//   gated   32 rows       177      215       428       713       2460        92
-//          192 rows       378      440       460       759       2027        65
-//   product 32 rows       111      117       196       315       1052        42
-//          128 rows       120      153       185       252        832        32
-//          256 rows       124      206       138       287        691        25
-// (96 experts at mean 43, product: 18.1, 14.6 and 20.1.)  One token over 8 of
-// 32 experts leaves 128 blocks (gated): K split over 2 groups of waves 60 us,
-// one group 92 us.
+// them, and by how many blocks come of it (16 rows against 256 weight rows each
+// where rows are few; partial tiles counted as half of the experts that can
+// have rows).  Measured, uniform routing, us; L: 32 experts, K = 7168 and 4096
+// (gated) or 2048 weight rows; S: 96 experts, K = 1024, 768 or 384; 1: one
+// expert as L, its mean rows in brackets.
+//   mean rows                 L 1/4   L 8  L 128  L 256  L 1024   S 85  S 171   1 (8)   1 (64)
+//   gated   16 rows, 2 of K     59   194    664   1208    3902      -      -      30       31
+//           32 rows             93   180    400    697    2381     43     74      38       39
+//           128-row tile       134   279    411    614    1927     40     59      80       80
+//   product 16 rows, 8 of K     23    92    438    790    2945     73    129      12       12
+//           32 rows             29   111    198    317    1041     28     36      25       30
+//           128-row tile        51   116    188    256     742     17     32      49       52
+//           256-row tile        83   124    136    289     677     22     25      80       85
+// With 96 blocks and more the split of K in 8 loses (K = 2048, 7168 weight rows,
+// 8 rows of 8 experts: 37, 32 rows 31, 16 rows with K in 2 parts 27), and so do
+// tiles that leave CUs idle (one expert, 512 rows: 62 and 109 against 33; gated
+// 95 against 49).
 template <bool GATED>
 hipError_t launch_product(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                           const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
     const int64_t mean = s.rows / s.E, cols = GATED ? s.N / 128 : (s.N + 255) / 256;
-    const auto tiles = [&](int BM) { return (s.rows / BM + 1) * cols; };
+    const int64_t used = s.rows < s.E ? s.rows : s.E;
+    const auto tiles = [&](int BM) { return (2 * (s.rows / BM) + used) * cols / 2; };
+    const int64_t blocks = (s.rows / 16 + used) * cols;
     if constexpr (GATED) {
-        if (mean >= 160 && tiles(192) >= 192)
-            return launch_gated_tile(s, offset, a, as, w, ws, q, qs, stream);
+        if (mean >= 140 && tiles(128) >= 160) return launch_gated_tile(s, offset, a, as, w, ws, q, qs, stream);
+        if (blocks < 256) return launch_stream<1, 8, 2, true>(s, offset, a, as, w, ws, out, q, qs, stream);
     } else {
-        if (mean >= 96 && tiles(256) >= 192)
-            return launch_tile<256>(s, offset, a, as, w, ws, out, stream);
-        if (mean >= 40 && tiles(128) >= 192)
-            return launch_tile<128>(s, offset, a, as, w, ws, out, stream);
+        if (mean >= 96 && tiles(256) >= 192) return launch_tile<256>(s, offset, a, as, w, ws, out, stream);
+        if (mean >= 40 && tiles(128) >= 128) return launch_tile<128>(s, offset, a, as, w, ws, out, stream);
+        if (blocks < 96) return launch_stream<1, 2, 8, false>(s, offset, a, as, w, ws, out, q, qs, stream);
+        if (blocks < 256 && mean < 16)
+            return launch_stream<1, 8, 2, false>(s, offset, a, as, w, ws, out, q, qs, stream);
     }
-    if (mean < 16 && (s.rows < s.E ? s.rows : s.E) * cols < 512)
-        return launch_stream<1, 2, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
-    return launch_stream<2, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
+    return launch_stream<2, 8, 1, GATED>(s, offset, a, as, w, ws, out, q, qs, stream);
 }
 
 }  // namespace

@@ -15,7 +15,7 @@ int check_router(const ep_router *r, int64_t T, ep::Router *out) {
     if (!r) return EP_EINVAL;
     if (r->num_experts < 1 || r->num_experts > 4096) return EP_EINVAL;
     if (r->num_topk < 1 || r->num_topk > 32 || r->num_topk > r->num_experts) return EP_EINVAL;
-    if (T < 0 || T * (int64_t)r->num_topk >= (int64_t(1) << 31)) return EP_EINVAL;
+    if (T < 0 || T >= (int64_t(1) << 26) || T * (int64_t)r->num_topk >= (int64_t(1) << 31)) return EP_EINVAL;
     if (r->score != EP_SCORE_SOFTMAX && r->score != EP_SCORE_SIGMOID) return EP_EINVAL;
     if (r->num_groups < 1 || r->num_groups > 64 || r->num_experts % r->num_groups != 0) return EP_EINVAL;
     if (r->topk_groups < 1 || r->topk_groups > r->num_groups) return EP_EINVAL;

@@ -10,8 +10,7 @@
 //
 // Scores, keys and sums are binary64.  The choice between two experts is a
 // comparison of scores that may differ by less than a binary32 rounding, and
-// one wrong comparison is a wrong index; at E = 256 the binary64 exponentials
-// are a few microseconds of the chip's time at 8192 tokens.
+// one wrong comparison is a wrong index.
 #include "ep_device.h"
 #include "moe.h"
 
@@ -143,8 +142,10 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t row, int
 // small batch is the chain of dependent steps in a wave, so the reductions are
 // register moves: the largest upper halves of the keys by a maximum over the
 // wave, ties by the lower halves, the first lane of those left by a ballot.
-// (One token, 256 experts, 8 groups: 11.0 us with reductions through LDS
-// shuffles and the groups scanned from LDS, EP_ROUTE_US us so.)
+// One token, 256 experts in 8 groups: a call every 5.4 us on the GPU; with the
+// reductions through LDS shuffles and the groups scanned from LDS 11.7.  8192
+// tokens (8.4 MB of logits): 15.8 us against 26, where the binary64 exponentials
+// and the k rounds of selection, some 8 waves on each SIMD, are what it costs.
 template <int EPL>
 __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_kernel(Router r, const void *logits, const float *bias,
                                                                     int64_t *topk_idx, float *topk_w, bool vec) {

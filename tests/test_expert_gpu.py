@@ -271,3 +271,13 @@ def test_few_rows_every_length(ep, K):
         off = _offsets(counts)
         _check_product(ep, off, *_draw(rng, off[-1] + 2, len(counts), K, N))
         _check_gated(ep, off, *_draw(rng, off[-1] + 2, len(counts), K, 512))
+
+
+@pytest.mark.parametrize("K", [128, 256, 896, 1024, 1152, 2176])
+def test_one_expert_few_rows(ep, K):
+    """A dense layer's few rows: K split over eight groups of waves, lengths shorter and longer than the groups."""
+    rng = np.random.default_rng(K + 1)
+    for rows, N in ((1, 8), (3, 72), (17, 520), (70, 264)):
+        x = _draw(rng, rows + 3, 1, K, N)
+        _check_product(ep, [2, rows + 2], *x)
+    _check_gated(ep, [1, 18], *_draw(rng, 20, 1, K, 512))

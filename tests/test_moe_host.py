@@ -201,3 +201,16 @@ def test_reference_e4m3_against_torch():
     b = np.arange(256, dtype=np.uint8)
     want = torch.from_numpy(b).view(torch.float8_e4m3fn).double().numpy()
     np.testing.assert_array_equal(moe_ref.e4m3_value(b), want)
+
+
+def test_grid_limits(lib):
+    """Shapes whose launch would pass the grid's limits are refused, ones just below are not (an odd output
+    pointer tells an accepted shape from a refused one without a launch)."""
+    r = _router()
+    assert lib.ep_route(ctypes.byref(_router(k=1)), 2 ** 26, FAKE, None, FAKE, FAKE, None) == ep.EP_EINVAL
+    assert lib.ep_route_backward(ctypes.byref(r), 2 ** 26, FAKE, FAKE, FAKE, FAKE, None) == ep.EP_EINVAL
+    for rows, N, ok in ((2 ** 20, 7168, True), (2 ** 23, 7168, True), (2 ** 24, 7168, False), (2 ** 29, 256, False),
+                        (2 ** 20, 2 ** 20, False), (2 ** 25, 256, True)):
+        sh = _expert(rows=rows, E=64, K=128, N=N)
+        want = ep.EP_EALIGN if ok else ep.EP_EINVAL
+        assert lib.ep_expert_gemm(ctypes.byref(sh), *[FAKE] * 5, ODD, None) == want, (rows, N)
