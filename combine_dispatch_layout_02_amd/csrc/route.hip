@@ -211,6 +211,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_kernel(Router r, co
 #pragma unroll
             for (int i = 0; i < EPL; ++i)
                 if (lane * EPL + i < r.E) mine[lane * EPL + i] = order_value(key[i]);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // the wave's own keys: LDS keeps their order
             __builtin_amdgcn_wave_barrier();
             if (lane < r.G)
                 for (int i = 0; i < per; ++i) {

@@ -540,7 +540,8 @@ typedef struct ep_expert_shape {
  * experts without rows cost no weight traffic.  expert_offset stays on the
  * device: no count reaches the host.  It may also be a slice [e0 .. e1] of a
  * dispatch's expert_offset with the weights of those experts (one rank's
- * share); row numbers stay absolute.
+ * share): row numbers stay absolute, and for RANK_MAJOR rows the share is
+ * num_ranks = 1 with a and out the rank's own block of rank_capacity rows.
  *   expert_offset [E+1] int32, ascending; entries are clamped to [0, rows]
  *   a        [rows, K] e4m3, a_scales [rows, K/128] fp32: FP8_S128 rows, as
  *            ep_dispatch delivers or ep_quant_fp8_s128 makes them

@@ -281,3 +281,42 @@ def test_one_expert_few_rows(ep, K):
         x = _draw(rng, rows + 3, 1, K, N)
         _check_product(ep, [2, rows + 2], *x)
     _check_gated(ep, [1, 18], *_draw(rng, 20, 1, K, 512))
+
+
+def test_one_ranks_block_of_rank_major_rows(ep):
+    """One rank's share of RANK_MAJOR rows: its block alone, its experts' slice of the offsets, num_ranks 1."""
+    rng = np.random.default_rng(23)
+    off = _offsets([30, 5, 0, 70, 12, 9, 3, 25])
+    R, M = 4, 48   # rank 1's 70 rows pass its block, rank 3's do not fill theirs
+    a, a_s, w, w_s = _draw(rng, R * M, 8, 256, 256)
+    for r in range(R):
+        rows, mine = slice(r * M, (r + 1) * M), slice(2 * r, 2 * r + 2)
+        args = (off[2 * r:2 * r + 3], a[rows], a_s[rows], w[mine], w_s[mine])
+        _check_product(ep, *args, R=1, M=M)
+        _check_gated(ep, *args, R=1, M=M)
+
+
+@pytest.mark.parametrize("copies", [1, 900])   # few rows, and tiles of many
+def test_gate_far_below_zero(ep, copies):
+    """silu's lower tail, where e^-g leaves binary32: h keeps its precision down to the smallest values.
+
+    Every sum is one product, exact, so g and u are.  All of a row's h are equal: the byte is 448 and the scale h / 448.
+    Bounds: 4 steps of h and one each of the scale, the quotient and the product, twice; and where values fall
+    below 2^-126 half the smallest step of e^g (times g u) and of the scale (times 448)."""
+    depth = np.repeat(np.arange(80.0, 104.0, dtype=np.float32), copies)
+    rows = depth.size
+    a = torch.zeros((rows, 128), dtype=torch.uint8)
+    a[:, 0] = 0x38                                   # 1
+    w = torch.zeros((1, 256, 128), dtype=torch.uint8)
+    w[0, :128, 0] = 0xB8                             # -1: the gate
+    w[0, 128:, 0] = 0x38
+    u = np.float32(2.0 ** 20)
+    a_s = torch.from_numpy(depth)[:, None].contiguous()
+    w_s = torch.tensor([1.0, float(u)]).reshape(1, 2, 1)
+    off = torch.tensor([0, rows], dtype=torch.int32)
+    q, s = ep.expert_gated(off.cuda(), a.cuda(), a_s.cuda(), w.cuda(), w_s.cuda())
+    d = depth.astype(np.float64)
+    h = -d * np.exp(-d) / (1 + np.exp(-d)) * d * float(u)
+    got = moe_ref.e4m3_value(q.cpu().numpy()) * s.cpu().double().numpy()
+    tol = 16 * 2.0 ** -23 * np.abs(h) + 2.0 ** -149 * (d * d * float(u) + 448)
+    assert (np.abs(got - h[:, None]) <= tol[:, None]).all()
