@@ -141,6 +141,18 @@ __device__ __forceinline__ i32x8 lds_operand(const uint8_t *lo16, const uint8_t 
     return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
 }
 
+// A lane's 4 bf16 at columns 4 quad of one group of 16 columns (a) and of the
+// next (b), quad = lane / 16, become 8 of one of them: lanes of odd quads hand
+// over their a for the b of the quad before.  A store is then 16 bytes a lane
+// and 64 a row (with 8 and 32, 32768 rows of 7168 took 40 us more).
+__device__ __forceinline__ vec16 eight(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1) {
+    const auto s0 = __builtin_amdgcn_permlane16_swap(a0, b0, false, false);
+    const auto s1 = __builtin_amdgcn_permlane16_swap(a1, b1, false, false);
+    return vec16{s0[0], s1[0], s0[1], s1[1]};
+}
+// The first of those columns, from the first of a's group.
+__device__ __forceinline__ int column8(int quad) { return 16 * (quad & 1) + 8 * (quad >> 1); }
+
 // The rows of expert e in a and the output, clamped into [0, rows].
 __device__ __forceinline__ void expert_rows(const int32_t *off, const ExpertShape &s, int e, int *lo, int *hi) {
     const int rows = (int)s.rows;
@@ -456,31 +468,35 @@ __launch_bounds__(64 * CW * KS) void ep_expert_stream_kernel(
 
 constexpr int kTileThreads = 512, kTileN = 256;   // 8 waves; weight rows of a tile
 
-// One block: BM rows by 256 weight rows, 8 waves, 2 by 4.  Both operands of a block of K = 128 are
-// staged in LDS, 2 or 3 buffers in turn: the next blocks' loads are in flight
-// while this one is multiplied.
-// Bound by the vector instructions that scale (one fused multiply-add for every
-// value and block of K) and the operand reads beside the matrix instructions,
-// which are busy for 0.39 of the time: 32768 rows, 32 experts, K = 2048, 7168
-// weight rows 670 us, 1.44 PFLOP/s; its loads alone take about half of that.
+// One block: BM rows by 256 weight rows, 8 waves, 2 by 4.  Blocks of K = 128 of
+// both operands are staged in LDS: the weights in three buffers, two blocks on,
+// a's rows in three or, at 256 rows, two, which fills the LDS.
+// Bound by the latency of those loads: 32768 rows, 32 experts, K = 2048, 7168
+// weight rows 627 us, 1.53 PFLOP/s (weights one block on only 680).  Timed
+// apart, on the form before with 680 us: without the products 626, without the
+// loads 487, without the result's stores 571.
 template <int BM>
 __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
     uint16_t *out, int slots, int cols) {
     constexpr int WN = 2, WM = 4, NF = kTileN / WN / 16, MF = BM / WM / 16;
-    constexpr int STAGES = BM <= 128 ? 3 : 2;      // what fits 160 KiB of LDS
-    __shared__ __attribute__((aligned(16))) uint8_t buf0[(kTileN + BM) * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t buf1[(kTileN + BM) * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t buf2[STAGES == 3 ? (kTileN + BM) * 128 : 16];
-    __shared__ int found;
+    constexpr int XS = BM <= 128 ? 3 : 2;          // buffers of a's rows: what 160 KiB of LDS hold
+    __shared__ __attribute__((aligned(16))) uint8_t wbuf0[kTileN * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t wbuf1[kTileN * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t wbuf2[kTileN * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t xbuf0[BM * 128];
+    __shared__ __attribute__((aligned(16))) uint8_t xbuf1[BM * 128];
+    int *found = reinterpret_cast<int *>(xbuf0);   // before the buffers, which may fill the LDS to the byte
 
     // 8 row tiles by all columns at a time, a row tile's columns on one XCD
-    // (689 us; an eighth of the tiles to each XCD as the gated tiles have it 760)
+    // (an eighth of the tiles to each XCD, as the gated tiles have it, is slower: 760 us
+    // against 689; so are 8 row tiles by an eighth of the columns, 712 against 682)
     const int per = 8 * cols, sb = blockIdx.x / per, in = blockIdx.x % per;
     const int slot = sb * 8 + in % 8, ct = in / 8;
     if (slot >= slots) return;
     int e, row, end;
-    if (!find_tile(off, s, slot, BM, &found, &e, &row, &end)) return;
+    if (!find_tile(off, s, slot, BM, found, &e, &row, &end)) return;
+    __syncthreads();   // everyone has read it
 
     const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wn = wid % WN, wm = wid / WN;
@@ -503,14 +519,12 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
         xoff[p] = (uint32_t)min(srow + 64 * p, end - 1 - row) * (uint32_t)s.K + piece;
     const rsrc_t wb = buffer(w0), xb = buffer(a + (size_t)row * s.K);
 
-    constexpr int PIECES = (kTileN + BM) / 64;
-    static_assert(PIECES <= 15, "the waits' counts");
-    const auto stage = [&](uint8_t *buf, int kb, int p) {   // piece p of a block of K
-        const uint32_t past = kb < KB ? 0u : 0x80000000u;
-        if (p < kTileN / 64)
-            load_to_lds(wb, buf + p * 8192 + wid * 1024, woff[p] | past, kb * 128);
-        else
-            load_to_lds(xb, buf + p * 8192 + wid * 1024, xoff[p - kTileN / 64] | past, kb * 128);
+    constexpr int WP = kTileN / 64, XP = BM / 64, PIECES = WP + XP;
+    const auto stage_w = [&](uint8_t *buf, int kb, int p) {   // piece p of a block of K of the weights
+        load_to_lds(wb, buf + p * 8192 + wid * 1024, woff[p] | (kb < KB ? 0u : 0x80000000u), kb * 128);
+    };
+    const auto stage_x = [&](uint8_t *buf, int kb, int p) {   // and of a's rows
+        load_to_lds(xb, buf + p * 8192 + wid * 1024, xoff[p] | (kb < KB ? 0u : 0x80000000u), kb * 128);
     };
 
     // scales: one register per lane and group of 16 rows, one per wave (its 128
@@ -531,13 +545,13 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     };
     const uint32_t plo = (uint32_t)((quad ^ (r16 & 7)) << 4), phi = plo ^ 64;
     const uint32_t wlo = (uint32_t)(wn * 128 + r16) * 128 + plo, whi = wlo ^ 64;
-    const uint32_t xrow = (uint32_t)(kTileN + wm * 16 * MF + r16) * 128;
+    const uint32_t xrow = (uint32_t)(wm * 16 * MF + r16) * 128;
     const uint32_t xlo = xrow + plo, xhi = xrow + phi;
-    const auto multiply = [&](const uint8_t *buf, const float (&x)[MF], float c, const auto &between) {
+    const auto multiply = [&](const uint8_t *wbuf, const uint8_t *xbuf, const float (&x)[MF], float c, const auto &between) {
         i32x8 xf[MF];
 #pragma unroll
-        for (int m = 0; m < MF; ++m) xf[m] = lds_operand(buf + xlo + 2048 * m, buf + xhi + 2048 * m);
-        const auto weights = [&](int n) { return lds_operand(buf + wlo + 2048 * n, buf + whi + 2048 * n); };
+        for (int m = 0; m < MF; ++m) xf[m] = lds_operand(xbuf + xlo + 2048 * m, xbuf + xhi + 2048 * m);
+        const auto weights = [&](int n) { return lds_operand(wbuf + wlo + 2048 * n, wbuf + whi + 2048 * n); };
         const auto add = [&](int n, const f32x4 (&d)[MF]) {
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
@@ -573,15 +587,16 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
         }
         add(NF - 1, last);
     };
-    // The loads of the block STAGES - 1 on are issued a few at a time between
-    // the matrix instructions: all at once they fill the memory pipe's queue and
-    // every wave waits.  Past the last block they read past the buffer's end
-    // (zeros, no memory traffic), which keeps the counts of the waits.
-    const auto step = [&](const uint8_t *cur, uint8_t *next, int kb) {
+    // The loads of later blocks are issued a few at a time between the matrix
+    // instructions: all at once they fill the memory pipe's queue and every wave
+    // waits.  Past the last block they read past the buffer's end (zeros, no
+    // memory traffic), which keeps the counts of the waits.
+    const auto step = [&](const uint8_t *wcur, const uint8_t *xcur, uint8_t *wnext, uint8_t *xnext, int kb) {
         // this wave's part of the block has arrived, of what came later at most
-        // the loads of STAGES - 2 blocks are under way; then every wave's part,
-        // and the buffer of the block before is free
-        __builtin_amdgcn_s_waitcnt(0x0F70 | (STAGES - 2) * PIECES);
+        // the weights two blocks on (with three buffers of a's rows, and those)
+        // are under way; then every wave's part, and the buffers of the block
+        // before are free
+        __builtin_amdgcn_s_waitcnt(0x0F70 | (XS == 3 ? PIECES : WP));
         barrier_only();
         float x[MF];
         const float c = sw;
@@ -589,21 +604,41 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
         for (int m = 0; m < MF; ++m) x[m] = sx[m];
         scales(min(kb + 1, KB - 1));
         __builtin_amdgcn_sched_barrier(0);
-        multiply(cur, x, c, [&](int n) {
+        multiply(wcur, xcur, x, c, [&](int n) {
 #pragma unroll
-            for (int p = n * PIECES / NF; p < (n + 1) * PIECES / NF; ++p) stage(next, kb + STAGES - 1, p);
+            for (int p = n * PIECES / NF; p < (n + 1) * PIECES / NF; ++p)
+                if (p < XP)
+                    stage_x(xnext, kb + XS - 1, p);
+                else
+                    stage_w(wnext, kb + 2, p - XP);
         });
     };
     scales(0);
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p) stage(buf0, 0, p);
-    if (STAGES == 3)
+    for (int p = 0; p < WP; ++p) stage_w(wbuf0, 0, p);
 #pragma unroll
-        for (int p = 0; p < PIECES; ++p) stage(buf1, 1, p);
-    for (int kb = 0; kb < KB; kb += STAGES) {
-        step(buf0, STAGES == 3 ? buf2 : buf1, kb);
-        if (kb + 1 < KB) step(buf1, buf0, kb + 1);
-        if (STAGES == 3 && kb + 2 < KB) step(buf2, buf1, kb + 2);
+    for (int p = 0; p < XP; ++p) stage_x(xbuf0, 0, p);
+    if (XS == 3)
+#pragma unroll
+        for (int p = 0; p < XP; ++p) stage_x(xbuf1, 1, p);
+#pragma unroll
+    for (int p = 0; p < WP; ++p) stage_w(wbuf1, 1, p);
+    if constexpr (XS == 3) {
+        __shared__ __attribute__((aligned(16))) uint8_t xbuf2[BM * 128];
+        for (int kb = 0; kb < KB; kb += 3) {
+            step(wbuf0, xbuf0, wbuf2, xbuf2, kb);
+            if (kb + 1 < KB) step(wbuf1, xbuf1, wbuf0, xbuf0, kb + 1);
+            if (kb + 2 < KB) step(wbuf2, xbuf2, wbuf1, xbuf1, kb + 2);
+        }
+    } else {
+        for (int kb = 0; kb < KB; kb += 6) {
+            step(wbuf0, xbuf0, wbuf2, xbuf1, kb);
+            if (kb + 1 < KB) step(wbuf1, xbuf1, wbuf0, xbuf0, kb + 1);
+            if (kb + 2 < KB) step(wbuf2, xbuf0, wbuf1, xbuf1, kb + 2);
+            if (kb + 3 < KB) step(wbuf0, xbuf1, wbuf2, xbuf0, kb + 3);
+            if (kb + 4 < KB) step(wbuf1, xbuf0, wbuf0, xbuf1, kb + 4);
+            if (kb + 5 < KB) step(wbuf2, xbuf1, wbuf1, xbuf0, kb + 5);
+        }
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);
 
@@ -616,9 +651,10 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
         for (int i = 0; i < 4 * NF; ++i) v[i] = acc[i / 4][m][i % 4];
         pack_bf16(v, o);
 #pragma unroll
-        for (int n = 0; n < NF; ++n) {
-            const int c = n0 + wn * 128 + 16 * n + 4 * quad;   // N % 8 == 0: all 4 in or all out
-            if (r < end && c < s.N) *reinterpret_cast<uint2 *>(out + (size_t)r * s.N + c) = uint2{o[2 * n], o[2 * n + 1]};
+        for (int n = 0; n < NF; n += 2) {
+            const vec16 v = eight(o[2 * n], o[2 * n + 1], o[2 * n + 2], o[2 * n + 3]);
+            const int c = n0 + wn * 128 + 16 * n + column8(quad);   // N % 8 == 0: all 8 in or all out
+            if (r < end && c < s.N) st16(out + (size_t)r * s.N + c, v);
         }
     }
 }

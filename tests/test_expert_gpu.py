@@ -320,3 +320,12 @@ def test_gate_far_below_zero(ep, copies):
     got = moe_ref.e4m3_value(q.cpu().numpy()) * s.cpu().double().numpy()
     tol = 16 * 2.0 ** -23 * np.abs(h) + 2.0 ** -149 * (d * d * float(u) + 448)
     assert (np.abs(got - h[:, None]) <= tol[:, None]).all()
+
+
+@pytest.mark.parametrize("K", [768, 896, 1024, 1664])
+@pytest.mark.parametrize("rows,E", [(13000, 24), (2500, 40)])
+def test_many_rows_product_every_buffer(ep, rows, E, K):
+    """Blocks of K past a whole turn of the tiles' buffers, by one to six of them."""
+    rng = np.random.default_rng(K + rows)
+    cuts = np.sort(rng.integers(0, rows + 1, E - 1)).tolist()
+    _check_product(ep, [0] + cuts + [rows], *_draw(rng, rows, E, K, 1032))
