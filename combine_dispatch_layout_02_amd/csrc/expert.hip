@@ -928,7 +928,7 @@ hipError_t launch_stream(const ExpertShape &s, const int32_t *offset, const uint
 //   product 16 rows, 8 of K     23    92    438    790    2945     73    129      12       12
 //           32 rows             29   111    198    317    1041     28     36      25       30
 //           128-row tile        51   116    188    256     742     17     32      49       52
-//           256-row tile        83   124    136    289     677     22     25      80       85
+//           256-row tile        83   124    127    273     647     22     25      80       85
 // With 96 blocks and more the split of K in 8 loses (K = 2048, 7168 weight rows,
 // 8 rows of 8 experts: 37, 32 rows 31, 16 rows with K in 2 parts 27), and so do
 // tiles that leave CUs idle (one expert, 512 rows: 62 and 109 against 33; gated
