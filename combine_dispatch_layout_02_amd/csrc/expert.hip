@@ -204,17 +204,27 @@ __device__ __forceinline__ float gate(float g, float u) {
     return g * (g >= 0.0f ? r : x * r) * u;
 }
 
-// Four values over a scale >= their largest magnitude / 448, as e4m3 bytes.  The
-// quotients are those of the IEEE division (a correctly rounded reciprocal and
-// one correction of the quotient by its remainder; at the ends of the range the
-// division itself), a third of its instructions; they stay below 464, from
-// where the conversion would not round to 448.
+// A group's scale: its largest magnitude / 448, 1 for zeros.  Where the quotient
+// would round to 0 it is the smallest subnormal, so that the bytes still hold h
+// to e4m3's precision and nothing is divided by 0.
+__device__ __forceinline__ float group_scale(float top) { return top == 0.0f ? 1.0f : fmaxf(top / 448.0f, 0x1p-149f); }
+
+// Four values over their group's scale, as e4m3 bytes.  The quotients are those
+// of the IEEE division: a correctly rounded reciprocal and one correction of the
+// quotient by its remainder, a third of its instructions, and at the ends of the
+// range the division itself.  The conversion makes NaN of what would round past
+// 448.  A normal scale is within half a step of the largest magnitude / 448, so
+// quotients stay below 464 and round to 448 at most; a subnormal one may have
+// lost a third of its value, so there they are clamped (a NaN stays).
 struct Divisor {
     float scale, inv;
     bool plain;
     __device__ __forceinline__ explicit Divisor(float s) : scale(s), inv(1.0f / s), plain(s > 0x1p-100f && s < 0x1p100f) {}
     __device__ __forceinline__ float over(float h) const {
-        if (!plain) return h / scale;
+        if (!plain) {
+            const float q = h / scale;
+            return q > 448.0f ? 448.0f : (q < -448.0f ? -448.0f : q);
+        }
         const float q = h * inv;
         return __builtin_fmaf(__builtin_fmaf(-q, scale, h), inv, q);
     }
@@ -455,7 +465,7 @@ __launch_bounds__(64 * CW * KS) void ep_expert_stream_kernel(
             float top = 0.0f;
 #pragma unroll
             for (int c = 0; c < CW; ++c) top = fmaxf(top, amax[c][16 * m + r16]);
-            const float scale = (top == 0.0f) ? 1.0f : top / 448.0f;
+            const float scale = group_scale(top);
             if (r >= end) continue;
             *reinterpret_cast<uint32_t *>(oq + (size_t)r * s.N + n0 + 4 * quad) =
                 Divisor(scale).quantise(h[m][0], h[m][1], h[m][2], h[m][3]);
@@ -862,7 +872,7 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_gated_tile_kernel(
     for (int m = 0; m < 2; ++m) {
         const int i = wm * 64 + 32 * m + r32, r = row + i;
         const float top = fmaxf(fmaxf(amax[0][i], amax[1][i]), fmaxf(amax[2][i], amax[3][i]));
-        const float scale = (top == 0.0f) ? 1.0f : top / 448.0f;
+        const float scale = group_scale(top);
         if (r >= end) continue;
         uint8_t *o = oq + (size_t)r * s.N + ct * 128 + wn * 32 + 4 * half;
         const Divisor by(scale);

@@ -561,7 +561,9 @@ int ep_expert_gemm(const ep_expert_shape *shape, const int32_t *expert_offset, c
  *     h[s, n] = g / (1 + exp(-g)) * u
  * leaves as FP8_S128 rows by ep_quant_fp8_s128's rule on the fp32 values (per
  * 128 elements scale = amax / 448, 1 for an all-zero group; e4m3_rne_sat(h /
- * scale)): the next ep_expert_gemm takes them as they are.
+ * scale)): the next ep_expert_gemm takes them as they are.  A scale that would
+ * round to 0 is the smallest subnormal, 2^-149, instead; where it is subnormal
+ * its own rounding can take elements past 448 scales, and those saturate.
  *   w        [E, 2 N, K] e4m3: N gate rows, then N up rows;
  *   w_scales [E, 2 N / 128, K/128] fp32
  *   out_q    [rows, N] e4m3 (16-byte aligned), out_scales [rows, N/128] fp32
