@@ -195,13 +195,17 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape 
 }
 
 // h = g / (1 + e^-g) u, for negative g as g e^g / (1 + e^g) u: what is divided
-// by lies in [1, 2], and h keeps its precision where e^-g passes binary32's
-// range.  The hardware's reciprocal is within one step, so h is off by 4 steps
-// at most: 1 of expf and of the reciprocal each, half of the sum and of the
-// three products each.
+// by lies in [1, 2].  Below -80, where e^g nears binary32's smallest values, it
+// is taken as the square of y = e^(g/2), with u multiplied in between: h keeps
+// its precision however small e^g is (1 + e^g is 1 there; y itself leaves the
+// normal range at g = -174, where |h| < 2^-116 for any u).  The hardware's
+// reciprocal is within one step, so h is off by 5 steps at most: 1 of expf (2 of
+// its square), 1 of the reciprocal, half of the sum and of the three products
+// each; and by half the smallest subnormal where h is subnormal itself.
 __device__ __forceinline__ float gate(float g, float u) {
-    const float x = expf(-__builtin_fabsf(g)), r = __builtin_amdgcn_rcpf(1.0f + x);
-    return g * (g >= 0.0f ? r : x * r) * u;
+    const bool deep = g < -80.0f;
+    const float x = expf(deep ? 0.5f * g : -__builtin_fabsf(g)), r = __builtin_amdgcn_rcpf(1.0f + x);
+    return deep ? g * x * u * x : g * (g >= 0.0f ? r : x * r) * u;
 }
 
 // A group's scale: its largest magnitude / 448, 1 for zeros.  Where the quotient

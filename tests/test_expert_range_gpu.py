@@ -74,3 +74,11 @@ def test_scales_down_to_the_smallest_subnormal(ep, copies):
     ups = np.concatenate([ups, 1.375 * ups[:14], -1.25 * ups[:14]])
     for gate in (1.0, -3.0, 40.0):
         _check(*_run(ep, np.full(ups.size, gate), ups, copies))
+
+
+@pytest.mark.parametrize("copies", [1, 300])
+@pytest.mark.parametrize("up,deepest", [(1.0, 116.0), (2.0 ** -6, 112.0), (2.0 ** 20, 130.0), (2.0 ** 100, 173.0)])
+def test_deep_gates(ep, up, deepest, copies):
+    """Every gate of a group far below zero, where e^g is subnormal or below all of binary32: h is not, or just so."""
+    gates = -np.linspace(78.0, deepest, 41)
+    _check(*_run(ep, gates, np.full(gates.size, up), copies))
