@@ -76,7 +76,12 @@ __device__ __forceinline__ double exp_below(float z, float top) {
     return z == top ? 1.0 : exp((double)z - (double)top);
 }
 
-__device__ __forceinline__ double sigmoid_f64(float z) { return 1.0 / (1.0 + exp(-(double)z)); }
+// e^-z leaves binary64 near z = -710, e^z only near -745; 1 + e^z is 1 there.
+__device__ __forceinline__ double sigmoid_f64(float z) {
+    const bool low = z < -700.0f;
+    const double x = exp((double)(low ? z : -z));
+    return low ? x : 1.0 / (1.0 + x);
+}
 
 // A binary64 as an unsigned integer of the same order (-0 below +0; the keys
 // hold no -0: p >= +0 and p + bias rounds to +0).
