@@ -83,6 +83,11 @@ __device__ __forceinline__ double sigmoid_f64(float z) {
     return low ? x : 1.0 / (1.0 + x);
 }
 
+// Below this the taken scores may be subnormal and their shares inexact; a score
+// then is e^z times the same factor for all of them (for a sigmoid 1, as 1 + e^z
+// is 1), and the shares come from the exponentials over the largest of them.
+constexpr double kVanishing = 0x1p-960;
+
 // A binary64 as an unsigned integer of the same order (-0 below +0; the keys
 // hold no -0: p >= +0 and p + bias rounds to +0).
 __device__ __forceinline__ uint64_t order_bits(double v) {
@@ -292,7 +297,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_kernel(Router r, co
     double weight = r.softmax ? score / total : score;
     if (r.renorm) {   // the softmax's common sum cancels
         double sum = wave_sum_f64(score);
-        if (r.softmax && !(sum > 0.0)) {   // the taken experts' scores all vanish against the largest
+        if (sum < kVanishing && (r.softmax || sum > 0.0)) {   // shares of e^z
             const float zt = taken >= 0 ? load_logit(logits, row + taken, r.bf16) : -inf;
             const float m = wave_max_f32(zt);
             score = taken >= 0 ? exp_below(zt, m) : 0.0;
@@ -367,8 +372,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_backward_kernel(Rou
         const double hi = 1.0 / (1.0 + x), lo = x / (1.0 + x);
         const double p = taken >= 0 ? (zt >= 0 ? hi : lo) : 0.0, rest = zt >= 0 ? lo : hi;
         if (r.renorm) {
-            const double sum = wave_sum_f64(p);
-            const double q = sum > 0.0 ? p / sum : 0.0;
+            double part = p, sum = wave_sum_f64(p);
+            if (sum > 0.0 && sum < kVanishing) {   // shares of e^z, as in the forward pass
+                const float m = wave_max_f32(taken >= 0 ? zt : -inf);
+                part = taken >= 0 ? exp_below(zt, m) : 0.0;
+                sum = wave_sum_f64(part);
+            }
+            const double q = sum > 0.0 ? part / sum : 0.0;
             const double mean = wave_sum_f64(taken >= 0 ? g * q : 0.0);
             dz = taken >= 0 ? (g - mean) * q * rest : 0.0;
         } else {

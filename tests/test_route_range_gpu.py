@@ -20,6 +20,12 @@ def ep():
     return mod
 
 
+def _shares(z):
+    """e^z over its sum, in 64 bits: what renormalised weights are where 1 + e^z is 1, and for a softmax always."""
+    e = np.exp(z - z.max(1, keepdims=True))
+    return e / e.sum(1, keepdims=True)
+
+
 def _low_logits(E):
     """Logits where e^-z has left binary64 (from -709.8 on) and e^z has not (until -745), and the three best experts."""
     z = np.full((4, E), -2000.0, np.float32)
@@ -36,3 +42,41 @@ def test_order_of_the_smallest_sigmoid_scores(ep, E):
     idx, w = ep.route(torch.from_numpy(z).cuda(), ep.make_router(E, 3, "sigmoid"))
     np.testing.assert_array_equal(idx.cpu().numpy(), want)
     assert (w == 0).all()                            # below all of binary32
+
+
+@pytest.mark.parametrize("E", [12, 1500])
+def test_shares_of_the_smallest_sigmoid_scores(ep, E):
+    z, want = _low_logits(E)
+    idx, w = ep.route(torch.from_numpy(z).cuda(), ep.make_router(E, 3, "sigmoid", renormalize=True))
+    np.testing.assert_array_equal(idx.cpu().numpy(), want)
+    ref = _shares(np.take_along_axis(z, want, 1).astype(np.float64))
+    assert (np.abs(w.cpu().double().numpy() - ref) <= F32_HALF * ref + 1e-12).all()
+
+
+@pytest.mark.parametrize("E", [40, 1500])
+def test_softmax_shares_of_experts_far_below_the_largest(ep, E):
+    """A bias takes experts whose scores are subnormal, or 0, against the largest logit; their shares stay exact."""
+    z = np.full((5, E), -3000.0, np.float32)
+    z[:, 0] = 0
+    z[:, 30:33] = [[-600, -601, -602.5], [-700, -701, -702.5], [-735, -737, -738.5], [-743, -744, -744.5],
+                   [-800, -801, -802]]
+    bias = torch.zeros(E)
+    bias[30:33] = torch.tensor([4.0, 3.0, 2.0])
+    r = ep.make_router(E, 3, "softmax", renormalize=True)
+    idx, w = ep.route(torch.from_numpy(z).cuda(), r, bias.cuda())
+    assert (idx.cpu() == torch.tensor([30, 31, 32])).all()
+    ref = _shares(z[:, 30:33].astype(np.float64))
+    assert (np.abs(w.cpu().double().numpy() - ref) <= F32_HALF * ref + 1e-12).all()
+
+
+@pytest.mark.parametrize("score", ("softmax", "sigmoid"))
+def test_gradient_of_shares_at_the_bottom_of_binary64(ep, score):
+    """With shares q the gradient is q (g - <g, q>): 1 - p is 1 here for a sigmoid."""
+    z = np.array([[-720, -715, -712], [-744, -743, -742.5], [-700, -709.5, -712], [-600, -602, -601]], np.float32)
+    g = np.array([[1, -2, 0.5], [3, 1, -1], [0.25, 1, 2], [1, 2, 3]], np.float32)
+    idx = torch.arange(3).repeat(4, 1)
+    r = ep.make_router(3, 3, score, renormalize=True)
+    dz = ep.route_backward(torch.from_numpy(g).cuda(), torch.from_numpy(z).cuda(), idx.cuda(), r)
+    q = _shares(z.astype(np.float64))
+    ref = q * (g - (g * q).sum(1, keepdims=True))
+    assert (np.abs(dz.cpu().double().numpy() - ref) <= F32_HALF * np.abs(ref) + 1e-12).all()
