@@ -71,6 +71,16 @@ __device__ __forceinline__ float load_logit(const void *z, int64_t i, bool bf16)
     return bf16 ? u2f((uint32_t) static_cast<const uint16_t *>(z)[i] << 16) : static_cast<const float *>(z)[i];
 }
 
+// binary64 -> bf16 in one rounding: what binary32 cannot hold becomes an odd last
+// bit of it (to odd, towards zero), 16 bits below bf16's, so the second rounding
+// sees on which side of a middle the value lies.
+__device__ __forceinline__ uint32_t f64_to_bf16(double v) {
+    const float f = (float)v;
+    uint32_t u = f2u(f);
+    if ((double)f != v && v == v) u = (u - (fabs((double)f) > fabs(v) ? 1u : 0u)) | 1u;
+    return f32_to_bf16(u2f(u));
+}
+
 // e^(z - top) with the limit at top = +inf: the experts at +inf share.
 __device__ __forceinline__ double exp_below(float z, float top) {
     return z == top ? 1.0 : exp((double)z - (double)top);
@@ -402,7 +412,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_backward_kernel(Rou
         const int e = i * kWave + lane;
         if (e >= r.E) continue;
         if (r.bf16)
-            static_cast<uint16_t *>(grad_logits)[row + e] = (uint16_t)f32_to_bf16((float)out[i]);
+            static_cast<uint16_t *>(grad_logits)[row + e] = (uint16_t)f64_to_bf16(out[i]);
         else
             static_cast<float *>(grad_logits)[row + e] = (float)out[i];
     }

@@ -80,3 +80,36 @@ def test_gradient_of_shares_at_the_bottom_of_binary64(ep, score):
     q = _shares(z.astype(np.float64))
     ref = q * (g - (g * q).sum(1, keepdims=True))
     assert (np.abs(dz.cpu().double().numpy() - ref) <= F32_HALF * np.abs(ref) + 1e-12).all()
+
+
+def _bf16_nearest(x):
+    """Positive binary64 values to the nearest bf16, ties to even, in one rounding."""
+    m, e = np.frexp(x)
+    return np.ldexp(np.rint(m * 256), e - 8)         # 8 bits; rint goes to even
+
+
+def test_bf16_gradient_is_rounded_once(ep):
+    """Gradients just above and just below the middle of two bf16 values, by less than a step of binary32."""
+    rng = np.random.default_rng(3)
+    g, s = rng.uniform(1, 2, 1 << 21).astype(np.float32), np.float32(1 + 5 * 2.0 ** -23)
+    x = g.astype(np.float64) * float(s) / 4          # z = 0: p (1 - p) = 1 / 4, exact
+    twice = _bf16_nearest(x.astype(np.float32).astype(np.float64))
+    g = np.concatenate([g[twice != _bf16_nearest(x)], [1 + 2.0 ** -8, 1 + 3 * 2.0 ** -8]]).astype(np.float32)
+    want = _bf16_nearest(g.astype(np.float64) * float(s) / 4)
+    assert g.size > 4                                # the draw holds such values
+    z = torch.zeros(g.size, 2, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(g.size, 1, dtype=torch.int64, device="cuda")
+    for sign in (1, -1):
+        r = ep.make_router(2, 1, "sigmoid", scale=sign * float(s))
+        dz = ep.route_backward(torch.from_numpy(g)[:, None].cuda(), z, idx, r).cpu().double().numpy()
+        np.testing.assert_array_equal(dz[:, 0], sign * want)
+        assert (dz[:, 1] == 0).all()
+    # the ends of bf16: subnormals, overflow, infinities and NaN
+    g = torch.tensor([2.0 ** -131, 1.25 * 2.0 ** -131, 3 * 2.0 ** -132, 2.0 ** -136, 3.3e38, math.inf, -math.inf,
+                      math.nan, 0.0]).cuda()
+    r = ep.make_router(2, 1, "sigmoid", scale=4.0)
+    dz = ep.route_backward(g[:, None].contiguous(), z[:9], idx[:9], r)[:, 0]
+    want = g.to(torch.bfloat16)
+    assert torch.equal(dz.isnan(), want.isnan()) and torch.equal(dz.nan_to_num(), want.nan_to_num())
+    r = ep.make_router(2, 1, "sigmoid", scale=8.0)
+    assert torch.isinf(ep.route_backward(g[4:5, None].contiguous(), z[:1], idx[:1], r)[0, 0])
