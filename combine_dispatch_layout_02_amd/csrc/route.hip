@@ -418,6 +418,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_backward_kernel(Rou
     }
 }
 
+// Waves of a block, a token each.  A launch holds fewer than 2^32 threads, so
+// the last batches below 2^26 tokens do not fill up blocks of 4.
+int token_waves(const Router &r, int most) { return r.T > (int64_t(1) << 26) - kRouteWaves ? 1 : most; }
+
 // Calls f with the experts-per-lane constant that holds E experts.
 template <typename F>
 hipError_t with_epl(int E, F f) {
@@ -434,7 +438,7 @@ hipError_t with_epl(int E, F f) {
 
 hipError_t launch_route(const Router &r, const void *logits, const float *bias, int64_t *topk_idx,
                         float *topk_w, hipStream_t stream) {
-    const int waves = r.E > 1024 ? 1 : kRouteWaves;
+    const int waves = token_waves(r, r.E > 1024 ? 1 : kRouteWaves);
     const bool vec = r.E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15u) == 0;
     const size_t lds = r.G > 1 ? sizeof(double) * (size_t)waves * r.E : 0;   // at most 32 KiB
     const dim3 grid((unsigned)((r.T + waves - 1) / waves)), block(kWave * waves);
@@ -447,7 +451,8 @@ hipError_t launch_route(const Router &r, const void *logits, const float *bias, 
 
 hipError_t launch_route_backward(const Router &r, const void *logits, const int64_t *topk_idx,
                                  const float *grad_topk_w, void *grad_logits, hipStream_t stream) {
-    const dim3 grid((unsigned)((r.T + kRouteWaves - 1) / kRouteWaves)), block(kWave * kRouteWaves);
+    const int waves = token_waves(r, kRouteWaves);
+    const dim3 grid((unsigned)((r.T + waves - 1) / waves)), block(kWave * waves);
     return with_epl(r.E, [&](auto epl) {
         hipLaunchKernelGGL(ep_route_backward_kernel<decltype(epl)::value>, grid, block, 0, stream, r, logits, topk_idx,
                            grad_topk_w, grad_logits);

@@ -113,3 +113,24 @@ def test_bf16_gradient_is_rounded_once(ep):
     assert torch.equal(dz.isnan(), want.isnan()) and torch.equal(dz.nan_to_num(), want.nan_to_num())
     r = ep.make_router(2, 1, "sigmoid", scale=8.0)
     assert torch.isinf(ep.route_backward(g[4:5, None].contiguous(), z[:1], idx[:1], r)[0, 0])
+
+
+@pytest.mark.parametrize("T", [2 ** 26 - 4, 2 ** 26 - 3, 2 ** 26 - 1])
+def test_largest_batches(ep, T):
+    """Every documented number of tokens: launches of up to 2^32 threads less some."""
+    z = torch.empty(T, 2, dtype=torch.bfloat16, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(1))
+    r = ep.make_router(2, 1, "softmax")
+    idx, w = ep.route(z, r)
+    assert torch.equal(idx[:, 0], (z[:, 1] > z[:, 0]).long())
+    d = (z[:, 0].double() - z[:, 1].double()).abs()
+    p = 1 / (1 + torch.exp(-d))
+    assert ((w[:, 0].double() - p).abs() <= F32_HALF * p + 1e-14).all()
+    del idx, w, p, d
+    g = torch.ones(T, 1, device="cuda")
+    idx = torch.zeros(T, 1, dtype=torch.int64, device="cuda")
+    dz = ep.route_backward(g, z, idx, r)
+    d = z[:, 0].double() - z[:, 1].double()
+    want = 1 / (1 + torch.exp(-d)) / (1 + torch.exp(d))
+    del d, idx, g
+    for i, sign in ((0, 1), (1, -1)):
+        assert ((dz[:, i].double() - sign * want).abs() <= BF16_HALF * (1 + 1e-6) * want + 2.0 ** -133).all()
