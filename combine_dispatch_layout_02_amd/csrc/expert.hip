@@ -13,6 +13,7 @@
 // the row's scale is one register per lane and the result one wide store.
 #include "ep_device.h"
 #include "moe.h"
+#include "tile_order.h"
 
 namespace ep {
 namespace {
@@ -721,13 +722,8 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_gated_tile_kernel(
     __shared__ int found;
     __shared__ float amax[WN][BM];
 
-    // consecutive blocks go to the 8 XCDs in turn; each XCD takes an eighth of
-    // the tiles, 8 row tiles by 4 columns together, which share their operands
-    // in its L2 (1929 us against 2043 with all columns of 2 row tiles together)
-    const int tile = (int)(blockIdx.x % 8) * (int)(gridDim.x / 8) + (int)(blockIdx.x / 8);
-    const int per = 8 * cols, in = tile % per, group = in / 32, wide = min(4, cols - 4 * group);
-    const int slot = tile / per * 8 + (in - 32 * group) / wide, ct = 4 * group + (in - 32 * group) % wide;
-    if (slot >= slots) return;
+    int slot, ct;
+    if (!TileOrder(slots, cols).tile(blockIdx.x, &slot, &ct)) return;
     int e, row, end;
     if (!find_tile(off, s, slot, BM, &found, &e, &row, &end)) return;
 
@@ -914,8 +910,7 @@ hipError_t launch_tile(const ExpertShape &s, const int32_t *offset, const uint8_
 hipError_t launch_gated_tile(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                              const uint8_t *w, const float *ws, uint8_t *q, float *qs, hipStream_t stream) {
     const int slots = (int)tile_slots(s, 128), cols = s.N / 128;
-    const int64_t blocks = (int64_t)((slots + 7) / 8) * 8 * cols;
-    hipLaunchKernelGGL(ep_expert_gated_tile_kernel, dim3((unsigned)blocks), dim3(kTileThreads), 0, stream, s, offset,
+    hipLaunchKernelGGL(ep_expert_gated_tile_kernel, dim3((unsigned)TileOrder(slots, cols).blocks()), dim3(kTileThreads), 0, stream, s, offset,
                        a, as, w, ws, q, qs, slots, cols);
     return hipGetLastError();
 }
