@@ -203,10 +203,29 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape 
 // reciprocal is within one step, so h is off by 5 steps at most: 1 of expf (2 of
 // its square), 1 of the reciprocal, half of the sum and of the three products
 // each; and by half the smallest subnormal where h is subnormal itself.
+template <bool DEEP>
 __device__ __forceinline__ float gate(float g, float u) {
-    const bool deep = g < -80.0f;
+    const bool deep = DEEP && g < -80.0f;
     const float x = expf(deep ? 0.5f * g : -__builtin_fabsf(g)), r = __builtin_amdgcn_rcpf(1.0f + x);
     return deep ? g * x * u * x : g * (g >= 0.0f ? r : x * r) * u;
+}
+// A lane's values; a wave without such gates does not pay for the choice (32
+// values a lane, 5 % of a tile's time at K = 1024).
+template <typename V>
+__device__ __forceinline__ V gates(V g, V u) {
+    constexpr int n = sizeof(V) / sizeof(float);
+    float least = g[0];
+#pragma unroll
+    for (int i = 1; i < n; ++i) least = fminf(least, g[i]);
+    V h;
+    if (__ballot(least < -80.0f) == 0) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) h[i] = gate<false>(g[i], u[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) h[i] = gate<true>(g[i], u[i]);
+    }
+    return h;
 }
 
 // A group's scale: its largest magnitude / 448, 1 for zeros.  Where the quotient
@@ -225,17 +244,22 @@ struct Divisor {
     float scale, inv;
     bool plain;
     __device__ __forceinline__ explicit Divisor(float s) : scale(s), inv(1.0f / s), plain(s > 0x1p-100f && s < 0x1p100f) {}
-    __device__ __forceinline__ float over(float h) const {
-        if (!plain) {
-            const float q = h / scale;
-            return q > 448.0f ? 448.0f : (q < -448.0f ? -448.0f : q);
-        }
+    __device__ __forceinline__ float corrected(float h) const {
         const float q = h * inv;
         return __builtin_fmaf(__builtin_fmaf(-q, scale, h), inv, q);
     }
+    __device__ __forceinline__ float clamped(float h) const {
+        const float q = h / scale;
+        return q > 448.0f ? 448.0f : (q < -448.0f ? -448.0f : q);
+    }
     __device__ __forceinline__ uint32_t quantise(float a, float b, float c, float d) const {
-        int v = __builtin_amdgcn_cvt_pk_fp8_f32(over(a), over(b), 0, false);
-        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(over(c), over(d), v, true);
+        if (plain) {
+            a = corrected(a), b = corrected(b), c = corrected(c), d = corrected(d);
+        } else {
+            a = clamped(a), b = clamped(b), c = clamped(c), d = clamped(d);
+        }
+        const int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
     }
 };
 
@@ -449,11 +473,9 @@ __launch_bounds__(64 * CW * KS) void ep_expert_stream_kernel(
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
                 float top = 0.0f;
+                h[m] = gates(acc[0][m], acc[1][m]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[m][i] = gate(acc[0][m][i], acc[1][m][i]);
-                    top = fmaxf(top, fabsf(h[m][i]));
-                }
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(h[m][i]));
                 top = fmaxf(top, __shfl_xor(top, 16));
                 tops[m] = fmaxf(top, __shfl_xor(top, 32));
             }
@@ -859,11 +881,9 @@ __global__ __launch_bounds__(kTileThreads) void ep_expert_gated_tile_kernel(
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
         float top = 0.0f;
+        acc[0][m] = gates(acc[0][m], acc[1][m]);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            acc[0][m][i] = gate(acc[0][m][i], acc[1][m][i]);
-            top = fmaxf(top, fabsf(acc[0][m][i]));
-        }
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(acc[0][m][i]));
         top = fmaxf(top, __shfl_xor(top, 32));
         if (half == 0) amax[wn][wm * 64 + 32 * m + r32] = top;
     }
