@@ -18,6 +18,8 @@
 namespace ep {
 namespace {
 
+constexpr int kTileThreads = 512, kTileN = 256;   // of the tiled forms: 8 waves; weight rows of a tile
+
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -193,6 +195,66 @@ __device__ __forceinline__ bool find_tile(const int32_t *off, const ExpertShape 
     *row = r0;
     *end = hi;
     return r0 >= lo && r0 < hi;   // offsets that do not ascend: no tile
+}
+
+// The tile of this block among those that have rows, in TileOrder's order: the
+// experts' tiles are counted and added up over the block, a run of experts per
+// thread, and the thread whose run holds the tile names it.  Offsets that do not
+// ascend: the counts saturate, and every row stays one of the buffer's.
+struct TileSearch {
+    int expert, row, end;
+    int sums[kTileThreads / kWave];   // of the waves
+};
+__device__ __forceinline__ bool order_tile(const int32_t *off, const ExpertShape &s, int BM, int cols,
+                                           TileSearch *found, int *expert, int *row, int *end, int *col) {
+    const auto add = [](int a, int b) { return min(a + b, 1 << 30); };
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wid = tid / kWave;
+    const int run = (s.E + kTileThreads - 1) / kTileThreads, e0 = tid * run, e1 = min(e0 + run, s.E);
+    int mine = 0, lo = 0, hi = 0;
+    for (int e = e0; e < e1; ++e) {
+        expert_rows(off, s, e, &lo, &hi);
+        mine = add(mine, (hi - lo + BM - 1) / BM);
+    }
+    // up to and with this thread: inside rows of 16 lanes, across them, across the waves
+    int upto = mine;
+    upto = add(upto, __builtin_amdgcn_update_dpp(0, upto, 0x111, 0xf, 0xf, false));
+    upto = add(upto, __builtin_amdgcn_update_dpp(0, upto, 0x112, 0xf, 0xf, false));
+    upto = add(upto, __builtin_amdgcn_update_dpp(0, upto, 0x114, 0xf, 0xf, false));
+    upto = add(upto, __builtin_amdgcn_update_dpp(0, upto, 0x118, 0xf, 0xf, false));
+    upto = add(upto, __builtin_amdgcn_update_dpp(0, upto, 0x142, 0xa, 0xf, false));
+    upto = add(upto, __builtin_amdgcn_update_dpp(0, upto, 0x143, 0xc, 0xf, false));
+    if (tid == 0) found->expert = -1;
+    if (lane == kWave - 1) found->sums[wid] = upto;
+    __syncthreads();
+    int total = 0, before = 0;
+#pragma unroll
+    for (int i = 0; i < kTileThreads / kWave; ++i) {
+        if (i == wid) before = total;
+        total = add(total, found->sums[i]);
+    }
+    upto = add(upto, before);
+    total = __builtin_amdgcn_readfirstlane(total);
+    int slot;
+    if (!TileOrder{total, cols}.tile(blockIdx.x, &slot, col)) return false;   // the same for the whole block
+    int at = upto - mine;
+    if (slot >= at && slot < upto) {
+        int e = e0;
+        if (run > 1)   // else lo and hi are the expert's
+            for (; e < e1; ++e) {
+                expert_rows(off, s, e, &lo, &hi);
+                const int n = (hi - lo + BM - 1) / BM;
+                if (slot - at < n) break;
+                at += n;
+            }
+        found->expert = min(e, s.E - 1);
+        found->row = lo + (slot - at) * BM;
+        found->end = hi;
+    }
+    __syncthreads();
+    *expert = __builtin_amdgcn_readfirstlane(found->expert);
+    *row = __builtin_amdgcn_readfirstlane(found->row);
+    *end = __builtin_amdgcn_readfirstlane(found->end);
+    return *expert >= 0 && *row >= 0 && *row < *end;
 }
 
 // h = g / (1 + e^-g) u, for negative g as g e^g / (1 + e^g) u: what is divided
@@ -503,7 +565,6 @@ __launch_bounds__(64 * CW * KS) void ep_expert_stream_kernel(
 
 // ---------------------------------------------------------------- many rows
 
-constexpr int kTileThreads = 512, kTileN = 256;   // 8 waves; weight rows of a tile
 
 // One block: BM rows by 256 weight rows, 8 waves, 2 by 4.  Blocks of K = 128 of
 // both operands are staged in LDS: the weights in three buffers, two blocks on,
@@ -736,18 +797,16 @@ __device__ __forceinline__ int place32(int r) { return ((r >> 1) & 1) | ((r >> 2
 // 1910 us, 1.0 PFLOP/s; with 16 x 16 x 32 instructions 2040 us.
 __global__ __launch_bounds__(kTileThreads) void ep_expert_gated_tile_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
-    uint8_t *oq, float *oqs, int slots, int cols) {
+    uint8_t *oq, float *oqs, int cols) {
     constexpr int BM = 128, WN = 4, PIECES = (kTileN + BM) / 64, BYTES = (kTileN + BM) * 128;
     __shared__ __attribute__((aligned(16))) uint8_t buf0[BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t buf1[BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t buf2[BYTES];
-    __shared__ int found;
+    __shared__ TileSearch found;
     __shared__ float amax[WN][BM];
 
-    int slot, ct;
-    if (!TileOrder(slots, cols).tile(blockIdx.x, &slot, &ct)) return;
-    int e, row, end;
-    if (!find_tile(off, s, slot, BM, &found, &e, &row, &end)) return;
+    int row, ct, e, end;
+    if (!order_tile(off, s, BM, cols, &found, &e, &row, &end, &ct)) return;
 
     const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wn = wid % WN, wm = wid / WN;
@@ -930,8 +989,8 @@ hipError_t launch_tile(const ExpertShape &s, const int32_t *offset, const uint8_
 hipError_t launch_gated_tile(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                              const uint8_t *w, const float *ws, uint8_t *q, float *qs, hipStream_t stream) {
     const int slots = (int)tile_slots(s, 128), cols = s.N / 128;
-    hipLaunchKernelGGL(ep_expert_gated_tile_kernel, dim3((unsigned)TileOrder(slots, cols).blocks()), dim3(kTileThreads), 0, stream, s, offset,
-                       a, as, w, ws, q, qs, slots, cols);
+    hipLaunchKernelGGL(ep_expert_gated_tile_kernel, dim3((unsigned)TileOrder::blocks(slots, cols)), dim3(kTileThreads), 0, stream, s, offset,
+                       a, as, w, ws, q, qs, cols);
     return hipGetLastError();
 }
 
