@@ -1003,24 +1003,29 @@ hipError_t launch_stream(const ExpertShape &s, const int32_t *offset, const uint
     return hipGetLastError();
 }
 
-// Which form: by the rows of an expert on average, all that the host knows of
-// them, and by how many blocks come of it (16 rows against 256 weight rows each
-// where rows are few; partial tiles counted as half of the experts that can
-// have rows).  Measured, uniform routing, us; L: 32 experts, K = 7168 and 4096
-// (gated) or 2048 weight rows; S: 96 experts, K = 1024, 768 or 384; 1: one
-// expert as L, its mean rows in brackets.
-//   mean rows                 L 1/4   L 8  L 128  L 256  L 1024   S 85  S 171   1 (8)   1 (64)
-//   gated   16 rows, 2 of K     59   194    664   1208    3902      -      -      30       31
-//           32 rows             93   180    400    697    2381     43     74      38       39
-//           128-row tile       134   279    411    614    1927     40     59      80       80
-//   product 16 rows, 8 of K     23    92    438    790    2945     73    129      12       12
-//           32 rows             29   111    198    317    1041     28     36      25       30
-//           128-row tile        51   116    188    256     742     17     32      49       52
-//           256-row tile        83   124    127    273     647     22     25      80       85
-// With 96 blocks and more the split of K in 8 loses (K = 2048, 7168 weight rows,
-// 8 rows of 8 experts: 37, 32 rows 31, 16 rows with K in 2 parts 27), and so do
-// tiles that leave CUs idle (one expert, 512 rows: 62 and 109 against 33; gated
-// 95 against 49).
+// Which form: by the rows of an expert on average, as if they filled the buffer
+// (the host knows no counts), and by how many blocks come of it (16 rows against
+// 256 weight rows each where rows are few; partial tiles counted as half of the
+// experts that can have rows).  Measured, uniform routing, us; L: 32 experts, K =
+// 7168 and 4096 (gated) or 2048 weight rows; S: 96 experts, K = 1024, 768 weight
+// rows; 1: one expert as L, its mean rows in brackets.
+//   mean rows               L 1/4   L 8  L 128  L 256  L 1024   S 85  S 171   1 (8)  1 (64)  1 (512)
+//   gated   16 rows, 2 of K    55   191    678   1241    4002     89    147      31      31       64
+//           32 rows            90   170    405    691    2343     44     75      39      39       44
+//           128-row tile       89   232    358    576    1908     41     63      78      79       83
+//   product 16 rows, 8 of K    26    90    443    807    2996    148    272      12      13       44
+//           16 rows, 2 of K    47   114    349    629    2014     85    133      29      29       32
+//           32 rows            47   108    197    318     997     43     73      29      31       31
+//           128-row tile       64   120    176    249     709     30     47      49      50       60
+//           256-row tile       90   122    130    258     629     38     45      77      78       94
+// Gated tiles start at 64 rows: 32 rows against tiles at 48, 64 and 96 rows, L 221
+// and 236, 261 and 238, 341 and 249; 64 experts, K = 2048, 2816 weight rows at 64
+// and 96 rows 146 and 112, 199 and 117; 256 experts as L at 32, 64 and 128 rows
+// 1555 and 1821, 1988 and 1920, 3070 and 2809.
+// With 96 blocks and more the split of K in 8 loses where K is short (K = 2048,
+// 7168 weight rows, 8 rows of 8 experts: 37, 32 rows 31, 16 rows with K in 2 parts
+// 27); where it is long it would still gain (product L 8), which the rule leaves,
+// as it leaves the 4 % of product L 256.
 template <bool GATED>
 hipError_t launch_product(const ExpertShape &s, const int32_t *offset, const uint8_t *a, const float *as,
                           const uint8_t *w, const float *ws, uint16_t *out, uint8_t *q, float *qs, hipStream_t stream) {
@@ -1029,7 +1034,7 @@ hipError_t launch_product(const ExpertShape &s, const int32_t *offset, const uin
     const auto tiles = [&](int BM) { return (2 * (s.rows / BM) + used) * cols / 2; };
     const int64_t blocks = (s.rows / 16 + used) * cols;
     if constexpr (GATED) {
-        if (mean >= 140 && tiles(128) >= 160) return launch_gated_tile(s, offset, a, as, w, ws, q, qs, stream);
+        if (mean >= 64 && tiles(128) >= 160) return launch_gated_tile(s, offset, a, as, w, ws, q, qs, stream);
         if (blocks < 256) return launch_stream<1, 8, 2, true>(s, offset, a, as, w, ws, out, q, qs, stream);
     } else {
         if (mean >= 96 && tiles(256) >= 192) return launch_tile<256>(s, offset, a, as, w, ws, out, stream);
