@@ -339,8 +339,8 @@ struct Divisor {
 // blocks in flight and no barrier.  The rows of a are shared by the waves: XB
 // blocks of K at a time, two buffers, a barrier per change.
 // Bound by the weights' bytes: gated, 1024 rows over 256 experts, K = 7168,
-// 4096 weight rows (7.4 GB) 1195 us, 6.2 TB/s of the 6.8 a stream of reads
-// reaches; 8 rows of 8 experts (235 MB) 53 us, 4.4 TB/s, of which about 10 us
+// 4096 weight rows (7.4 GB) 1200 us, 6.2 TB/s of the 6.8 a stream of reads
+// reaches; 8 rows of 8 experts (235 MB) 55 us, 4.3 TB/s, of which about 10 us
 // are the launch, the first loads and the sum of the parts of K.
 template <int MT, int CW, int KS, bool GATED>
 __global__ __attribute__((amdgpu_waves_per_eu(4, 4)))
@@ -565,14 +565,13 @@ __launch_bounds__(64 * CW * KS) void ep_expert_stream_kernel(
 
 // ---------------------------------------------------------------- many rows
 
-
 // One block: BM rows by 256 weight rows, 8 waves, 2 by 4.  Blocks of K = 128 of
 // both operands are staged in LDS: the weights in three buffers, two blocks on,
 // a's rows in three or, at 256 rows, two, which fills the LDS.
 // Bound by the latency of those loads: 32768 rows, 32 experts, K = 2048, 7168
-// weight rows 627 us, 1.53 PFLOP/s (weights one block on only 680).  Timed
-// apart, on the form before with 680 us: without the products 626, without the
-// loads 487, without the result's stores 571.
+// weight rows 625 to 644 us on two cards, 1.5 PFLOP/s (weights one block on only
+// 680).  Timed apart, on the form before with 680 us: without the products 626,
+// without the loads 487, without the result's stores 571.
 template <int BM>
 __global__ __launch_bounds__(kTileThreads) void ep_expert_tile_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
@@ -792,9 +791,9 @@ __device__ __forceinline__ int place32(int r) { return ((r >> 1) & 1) | ((r >> 2
 // matrix instructions; beside 16 x 16 x 32 ones two of those are free, beside
 // 32 x 32 x 16 ones, half as many to issue, three (measured: 19.5 against 24
 // cycles).  Three buffers of LDS: two blocks of K are under way.
-// Bound by the 16-bit matrix instructions (busy for 0.58 of the time) with the
+// Bound by the 16-bit matrix instructions (busy for 0.59 of the time) with the
 // vector ones beside them: 32768 rows, 32 experts, K = 7168, 4096 weight rows
-// 1910 us, 1.0 PFLOP/s; with 16 x 16 x 32 instructions 2040 us.
+// 1890 to 1960 us on two cards, 1.0 PFLOP/s; with 16 x 16 x 32 instructions 2040.
 __global__ __launch_bounds__(kTileThreads) void ep_expert_gated_tile_kernel(
     ExpertShape s, const int32_t *off, const uint8_t *a, const float *as, const uint8_t *w, const float *ws,
     uint8_t *oq, float *oqs, int cols) {

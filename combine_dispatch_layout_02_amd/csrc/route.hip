@@ -164,7 +164,7 @@ __device__ __forceinline__ void load_logits(const void *logits, int64_t row, int
 // wave, ties by the lower halves, the first lane of those left by a ballot.
 // One token, 256 experts in 8 groups: a call every 5.4 us on the GPU; with the
 // reductions through LDS shuffles and the groups scanned from LDS 11.7.  8192
-// tokens (8.4 MB of logits): 15.8 us against 26, where the binary64 exponentials
+// tokens (8.4 MB of logits): 16 us against 26, where the binary64 exponentials
 // and the k rounds of selection, some 8 waves on each SIMD, are what it costs.
 template <int EPL>
 __global__ __launch_bounds__(64 * kRouteWaves) void ep_route_kernel(Router r, const void *logits, const float *bias,

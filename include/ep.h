@@ -534,8 +534,10 @@ typedef struct ep_expert_shape {
  * with fp32 accumulation, b ascending over the K / 128 blocks (in 2 or 8 parts
  * that are added in order at the end where rows are few).  The inner sums are
  * the 8-bit matrix instruction's: it adds 8 products at a time, cut below 2^-13
- * of the largest (1.5e-5 of a random block's sum, where half a step of the bf16
- * result is 2^-9 to 2^-8).  Deterministic for a shape.  e is the expert whose
+ * of the largest.  So a block's sum is off by less than 7 * 2^-13 of the sum of
+ * its products' magnitudes (by 1.5e-5 of itself for random values, where half a
+ * step of the bf16 result is 2^-9 to 2^-8; all of it can be lost where products
+ * that large cancel).  Deterministic for a shape.  e is the expert whose
  * segment holds row s; rows of no segment are neither read nor written, and
  * experts without rows cost no weight traffic.  expert_offset stays on the
  * device: no count reaches the host.  It may also be a slice [e0 .. e1] of a
@@ -543,11 +545,15 @@ typedef struct ep_expert_shape {
  * share): row numbers stay absolute, and for RANK_MAJOR rows the share is
  * num_ranks = 1 with a and out the rank's own block of rank_capacity rows.
  *   expert_offset [E+1] int32, ascending; entries are clamped to [0, rows]
+ * The kernel's form is chosen from rows / num_experts, as if the segments filled
+ * the rows: in a buffer far larger than what is in it, as for a slice, the same
+ * rows can take longer than in one of their own (32 of 256 experts, 1024 rows
+ * each: 2.1 against 1.9 ms; few rows for each expert: up to half more).
  *   a        [rows, K] e4m3, a_scales [rows, K/128] fp32: FP8_S128 rows, as
  *            ep_dispatch delivers or ep_quant_fp8_s128 makes them
  *   w        [E, N, K] e4m3, w_scales [E, ceil(N/128), K/128] fp32
  *   out      [rows, N] bf16: what ep_combine takes with y_format BF16
- * a, w and out are 16-byte aligned.
+ * a, w and out are 16-byte aligned; the output overlaps no input.
  */
 int ep_expert_gemm(const ep_expert_shape *shape, const int32_t *expert_offset, const uint8_t *a,
                    const float *a_scales, const uint8_t *w, const float *w_scales, uint16_t *out,
@@ -566,7 +572,8 @@ int ep_expert_gemm(const ep_expert_shape *shape, const int32_t *expert_offset, c
  * its own rounding can take elements past 448 scales, and those saturate.
  *   w        [E, 2 N, K] e4m3: N gate rows, then N up rows;
  *   w_scales [E, 2 N / 128, K/128] fp32
- *   out_q    [rows, N] e4m3 (16-byte aligned), out_scales [rows, N/128] fp32
+ *   out_q    [rows, N] e4m3 (16-byte aligned), out_scales [rows, N/128] fp32;
+ *            they overlap no input
  */
 int ep_expert_gated(const ep_expert_shape *shape, const int32_t *expert_offset, const uint8_t *a,
                     const float *a_scales, const uint8_t *w, const float *w_scales, uint8_t *out_q,
@@ -580,7 +587,8 @@ int ep_expert_gated(const ep_expert_shape *shape, const int32_t *expert_offset, 
  *     grad_topk_w[t, j]     = sum_h dy[t,h] * expert_out[s, h]   (fp32)
  * A slot outside [0, rows) is masked: its weight's gradient is 0.  Rows that no
  * slot names are left untouched.  The slots of a dispatch's handle are
- * distinct; a row that two slots name gets one of the two gradients.
+ * distinct; in a row that two slots name each element is one of the two
+ * gradients'.
  * (The dispatch's own backward pass is ep_combine with weights 1; that of
  * ep_combine_ranks is ep_dispatch_ranks_cached of dy.)
  *   dy [T, H] bf16; expert_out, grad_expert_out [rows, H] bf16; all 16-byte
