@@ -1,0 +1,537 @@
+// few.hip -- the whole experts' layer for a few tokens, for gfx950, in two
+// kernels:
+//
+//   h[t, j]  = w[t, j] silu(G_e x[t]) * (U_e x[t]),   e = topk_idx[t, j]
+//   y[t]     = residual[t] + sum_j D_e h[t, j]
+//
+// At this size each expert's weights serve a few rows, and their bytes are the
+// time: 3 H I of them for every expert that a token has, read once.  Both
+// kernels stream them through LDS by direct loads, 4 KiB (32 rows by 128
+// bytes) a wave and step, two steps ahead, without a barrier; the products run
+// in 16-bit matrix instructions, with e4m3 weights widened to bf16 (exactly)
+// on their way.  The weights are the first operand, the tokens' rows the
+// second, so a lane's 4 results lie at consecutive columns of one token.
+//
+// No expert's rows are gathered first: a block of the first kernel finds its
+// expert's tokens in topk_idx by itself, one lane to a token, and one extra
+// block writes down for the second kernel which expert has which rows.
+#include "dense.h"
+#include "ep_device.h"
+#include "stream_device.h"
+#include "tile_device.h"
+
+namespace ep {
+namespace {
+
+// ---------------------------------------------------------------- the segments
+
+// Which expert has which rows, for the second kernel: one block, experts
+// ascending, each one's tokens ascending, 16 a segment.
+constexpr int kPlanThreads = 256;
+struct Plan {
+    uint32_t used[128];              // a bit for every expert
+    uint16_t ids[kFewTokens * 32];   // topk_idx, 0xFFFF where masked
+    uint16_t list[kFewTokens * 32];  // the experts that are used
+    uint16_t first[kFewTokens * 32]; // segments, then the first of each
+    int total;
+};
+__device__ void make_plan(Plan &p, const FewShape &s, const int64_t *idx, int32_t *count, FewSegment *seg) {
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wid = tid / kWave, pairs = s.T * s.k;
+    if (tid < 128) p.used[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < pairs; i += kPlanThreads) {
+        const int64_t e = idx[i];
+        const bool ok = e >= 0 && e < s.E;
+        p.ids[i] = ok ? (uint16_t)e : 0xFFFF;
+        if (ok) atomicOr(&p.used[e >> 5], 1u << (e & 31));
+    }
+    __syncthreads();
+    const auto scan = [&](int v) {   // sum up to and with the lane
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+            const int u = __shfl_up(v, d);
+            if (lane >= d) v += u;
+        }
+        return v;
+    };
+    if (wid == 0) {
+        const uint32_t a = p.used[2 * lane], b = p.used[2 * lane + 1];
+        uint64_t bits = (uint64_t)b << 32 | a;
+        const int upto = scan(__popcll(bits));
+        int at = upto - __popcll(bits);
+        for (; bits; bits &= bits - 1) p.list[at++] = (uint16_t)(64 * lane + __builtin_ctzll(bits));
+        if (lane == kWave - 1) p.total = upto;
+    }
+    __syncthreads();
+    const int used = p.total;
+    const auto find = [&](int e) {   // the lane's token: its first slot with expert e, or -1
+        int j = -1;
+        if (lane < s.T)
+            for (int i = s.k - 1; i >= 0; --i)
+                if (p.ids[lane * s.k + i] == e) j = i;
+        return j;
+    };
+    for (int d = wid; d < used; d += kPlanThreads / kWave) {
+        const int n = __popcll(__ballot(find(p.list[d]) >= 0));
+        if (lane == 0) p.first[d] = (uint16_t)((n + 15) / 16);
+    }
+    __syncthreads();
+    if (wid == 0) {
+        int carry = 0;
+        for (int d = 0; d < used; d += kWave) {
+            const int n = d + lane < used ? p.first[d + lane] : 0, upto = scan(n);
+            if (d + lane < used) p.first[d + lane] = (uint16_t)(carry + upto - n);
+            carry += __shfl(upto, kWave - 1);
+        }
+        if (lane == 0) *count = carry;
+    }
+    __syncthreads();
+    for (int d = wid; d < used; d += kPlanThreads / kWave) {
+        const int e = p.list[d], j = find(e);
+        const uint64_t has = __ballot(j >= 0);
+        const int rank = __popcll(has & lanemask_lt()), n = __popcll(has);
+        for (int g = 0; g * 16 < n; ++g) {
+            FewSegment *o = seg + p.first[d] + g;
+            const bool in = j >= 0 && rank / 16 == g;
+            const uint64_t tokens = __ballot(in);
+            if (in) reinterpret_cast<uint16_t *>(o->pair)[rank % 16] = (uint16_t)(lane * s.k + j);
+            if (lane == 0) {
+                o->tokens = tokens;
+                o->expert = e;
+                o->rows = min(16, n - 16 * g);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- gate and up
+
+// One block: 16 columns of h (16 gate and the same 16 up rows of the weights)
+// for up to 16 MT tokens of one expert; NW waves, each with a part of K.  The
+// grid has a block column for every pair (t, j); the block whose pair is the
+// first of its expert's (or of the next 16 MT tokens of it) does the work.
+template <bool F8, int MT, int NW, int NB>
+__global__ __launch_bounds__(64 * NW) void ep_few_up_kernel(
+    FewShape s, const uint16_t *__restrict__ x, const int64_t *__restrict__ idx, const float *__restrict__ w,
+    const uint8_t *__restrict__ up, const float *__restrict__ ups, int32_t *count, FewSegment *seg,
+    uint16_t *__restrict__ h, int cols) {
+    typedef Step<F8, 2> S;
+    constexpr int KE = S::KE, C = S::CHUNKS;
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[NW * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[NW * 4096];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[NB > 2 ? NW * 4096 : 16];
+    static_assert(NB == 2 || NB == 3, "as many buffers");
+    const auto buf = [&](int j) { return j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : buf2); };
+    __shared__ int32_t rows_pair[16 * MT];
+    __shared__ float rows_w[16 * MT];
+    static_assert(sizeof(Plan) <= sizeof(buf0), "the plan uses the buffer");
+    static_assert(64 * NW == kPlanThreads, "the plan's block");
+
+    if (blockIdx.x == 0) {
+        make_plan(*reinterpret_cast<Plan *>(buf0), s, idx, count, seg);
+        return;
+    }
+    const int p = (blockIdx.x - 1) / cols, n0 = (int)((blockIdx.x - 1) % cols) * 16;
+    const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane & 15, quad = lane >> 4;
+
+    // the expert's tokens, a lane for each
+    const int64_t e64 = idx[p];
+    if (e64 < 0 || e64 >= s.E) return;
+    const int e = __builtin_amdgcn_readfirstlane((int)e64);
+    int j = -1;
+    float wt = 0.0f;
+    if (lane < s.T)
+        for (int i = 0; i < s.k; ++i)
+            if (idx[lane * s.k + i] == e) {
+                wt = j < 0 ? w[lane * s.k + i] : wt + w[lane * s.k + i];
+                j = j < 0 ? i : j;
+            }
+    const uint64_t has = __ballot(j >= 0);
+    const int rank = __popcll(has & lanemask_lt());
+    const uint64_t mine = __ballot(j >= 0 && lane * s.k + j == p);
+    if (mine == 0) return;   // a token's second slot with the expert
+    const int r0 = __popcll(has & (mine - 1));
+    if (r0 % (16 * MT) != 0) return;
+    const int rows = min(16 * MT, __popcll(has) - r0);
+    if (wid == 0 && j >= 0 && rank >= r0 && rank < r0 + rows) {
+        rows_pair[rank - r0] = lane * s.k + j;
+        rows_w[rank - r0] = wt;
+    }
+    __syncthreads();
+
+    const uint32_t kbytes = (uint32_t)s.H * (F8 ? 1 : 2);
+    const int KU = (s.H + KE - 1) / KE;
+    const int first = KU * wid / NW, n = KU * (wid + 1) / NW - first;
+
+    const uint8_t *we = up + (size_t)e * 2 * s.I * kbytes;
+    const int last = s.I - 1 - n0;   // columns past the end repeat the last one
+    const rsrc_t gb = buffer(we + (size_t)n0 * kbytes), ub = buffer(we + ((size_t)s.I + n0) * kbytes);
+    Stage<2> st;
+    const int srow = lane >> 3;
+    st.piece = (uint32_t)(((lane & 7) ^ srow) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st.off[i] = (uint32_t)min(srow + 8 * (i & 1), last) * kbytes;
+    const auto stage = [&](uint8_t *buf, int i) {
+        const uint32_t k = i < n ? (uint32_t)(first + i) * 128 : 0u;
+        st.go(gb, ub, buf + wid * 4096, k, i < n ? kbytes : 0u);
+    };
+    // the tokens' rows, straight into the operands' layout
+    const rsrc_t xb = buffer(x, (int64_t)s.T * s.H * 2);
+    uint32_t xoff[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+        xoff[m] = 16 * m + r16 < rows ? (uint32_t)(rows_pair[16 * m + r16] / s.k) * (uint32_t)s.H * 2 : kPast;
+    struct Values {
+        vec16 v[MT][C];
+        float scale[2];
+    };
+    const auto load_x = [&](int i, Values &to) {
+        const uint32_t k = (uint32_t)(first + i) * (KE * 2);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint32_t at = k + S::at(c, quad);
+                to.v[m][c] = load_16(xb, i < n && at < (uint32_t)s.H * 2 ? xoff[m] + at : kPast, 0);
+            }
+    };
+    const int KB = s.H / 128;   // scales of a row of blocks
+    const rsrc_t sb = buffer(F8 ? ups + (size_t)e * (2 * s.I / 128) * KB : nullptr, F8 ? (int64_t)(2 * s.I / 128) * KB * 4 : 0);
+    const uint32_t soff[2] = {(uint32_t)(n0 / 128) * KB * 4, (uint32_t)((s.I + n0) / 128) * KB * 4};
+    const auto scales = [&](int i, Values &to) {
+        if constexpr (F8)
+#pragma unroll
+            for (int g = 0; g < 2; ++g) to.scale[g] = load_f32(sb, soff[g], (uint32_t)min(first + i, KB - 1) * 4);
+    };
+
+    f32x4 acc[2][MT] = {};
+    const uint32_t plo = (uint32_t)(r16 * 128 + ((quad ^ (r16 & 7)) << 4));
+    const auto step = [&](uint8_t *buf, const Values &x, Values &next, int i) {
+        wait_step<NB, MT * C + (F8 ? 2 : 0), 4>(i);
+        const uint8_t *p = buf + wid * 4096;
+        const S a(p, plo);   // the operands are in registers: their place takes the step NB on
+        __builtin_amdgcn_sched_barrier(0);
+        load_x(i + 1, next);
+        scales(i + 1, next);
+        __builtin_amdgcn_sched_barrier(0);
+        stage(buf, i + NB);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (m > 0 && rows <= 16 * m) break;   // the same for the whole block
+            f32x4 d[2] = {F8 ? f32x4{} : acc[0][m], F8 ? f32x4{} : acc[1][m]};
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const bf16x8 b = __builtin_bit_cast(bf16x8, x.v[m][c]);
+                d[0] = mfma(a.a[0][c], b, d[0]);
+                d[1] = mfma(a.a[1][c], b, d[1]);
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    acc[g][m][q] = F8 ? __builtin_fmaf(d[g][q], x.scale[g], acc[g][m][q]) : d[g][q];
+        }
+    };
+    Values v[2];
+    stage(buf0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_x(0, v[0]);
+    scales(0, v[0]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 1; j < NB; ++j) stage(buf(j), j);
+    constexpr int TURN = NB % 2 ? 2 * NB : NB;
+    for (int i = 0; i < n; i += TURN) {
+#pragma unroll
+        for (int j = 0; j < TURN; ++j)
+            if (j == 0 || i + j < n) step(buf(j), v[j % 2], v[(j + 1) % 2], i + j);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+
+    // the parts of K are added in their order
+    __syncthreads();
+    static_assert((NW - 1) * 2 * MT * 1024 <= NW * 4096, "they fit");
+    f32x4 *part = reinterpret_cast<f32x4 *>(buf0);
+    if (wid > 0)
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) part[((wid - 1) * 2 * MT + m) * kWave + lane] = acc[m & 1][m >> 1];
+    __syncthreads();
+    if (wid > 0) return;
+#pragma unroll
+    for (int q = 0; q < NW - 1; ++q)
+#pragma unroll
+        for (int m = 0; m < 2 * MT; ++m) acc[m & 1][m >> 1] += part[(q * 2 * MT + m) * kWave + lane];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const f32x4 v = gates(acc[0][m], acc[1][m]);
+        const int r = 16 * m + r16, col = n0 + 4 * quad;
+        if (r >= rows || col >= s.I) continue;   // I % 8 == 0: all 4 in or all out
+        // h leaves as two bf16 parts, its upper 16 bits and the rounded rest:
+        // 2^-17 of it is lost, at 4 bytes a value that the caches hold
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float f = v[q] * rows_w[r];
+            hi[q] = f2u(f) & 0xFFFF0000u;
+            const bool finite = (hi[q] & 0x7F800000u) != 0x7F800000u;
+            lo[q] = finite ? f32_to_bf16(f - u2f(hi[q])) : 0u;
+        }
+        uint16_t *o = h + (size_t)rows_pair[r] * 2 * s.I + col;
+        *reinterpret_cast<uint2 *>(o) = uint2{hi[0] >> 16 | hi[1], hi[2] >> 16 | hi[3]};
+        *reinterpret_cast<uint2 *>(o + s.I) = uint2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
+    }
+}
+
+// ---------------------------------------------------------------- down
+
+// One block: 16 G columns of y for all tokens.  The steps of all segments (an
+// expert's rows of the weights by K = I, for up to 8 RT of its tokens) form one
+// list, and each of the NW waves takes an equal run of it, so that every block
+// and wave reads the same amount whatever the routing.  A token's two parts of h
+// are two columns of the matrix instruction's second operand: 8 tokens an
+// instruction.  When a segment ends, its sums go to the lanes that hold the
+// tokens' results; the waves' results are added in order at the end.
+template <bool F8, int RT, int TT, int G, int NW, int NB>
+__global__ __launch_bounds__(64 * NW) void ep_few_down_kernel(
+    FewShape s, const int32_t *__restrict__ count, const FewSegment *__restrict__ seg,
+    const uint16_t *__restrict__ h, const uint8_t *__restrict__ down, const float *__restrict__ downs,
+    const uint16_t *residual, uint16_t *y) {
+    typedef Step<F8, G> S;
+    constexpr int KE = S::KE, C = S::CHUNKS;
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[NW * G * 2048];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[NW * G * 2048];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[NB > 2 ? NW * G * 2048 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t buf3[NB > 3 ? NW * G * 2048 : 16];
+    static_assert(NB >= 2 && NB <= 4, "as many buffers");
+    const auto buf = [&](int j) {
+        return j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : (j % NB == 2 ? buf2 : buf3));
+    };
+
+    const int n0 = blockIdx.x * 16 * G;
+    const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane & 15, quad = lane >> 4, c8 = r16 & 7, part = r16 >> 3;
+    const uint32_t kbytes = (uint32_t)s.I * (F8 ? 1 : 2);
+    const int KU = (s.I + KE - 1) / KE;
+    const int total = *count * KU;
+    const int lo = (int)((int64_t)total * wid / NW), hi = (int)((int64_t)total * (wid + 1) / NW);
+
+    Stage<G> st;
+    const int srow = lane >> 3, last = s.H - 1 - n0;
+    st.piece = (uint32_t)(((lane & 7) ^ srow) << 4);
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) st.off[i] = (uint32_t)min(srow + 8 * i, last) * kbytes;
+    f32x4 acc[TT][G] = {};
+    if (lo < hi) {
+        // the weights' place in the list, two steps ahead
+        int wg = lo / KU, wu = lo % KU;
+        const auto weights = [&](int g) {
+            return buffer(down + ((size_t)seg[g].expert * s.H + n0) * kbytes);
+        };
+        rsrc_t wb = weights(wg);
+        const auto stage = [&](uint8_t *buf, int i) {   // steps lo, lo + 1, ... in turn
+            st.go(wb, wb, buf + wid * (G * 2048), (uint32_t)wu * 128, i < hi ? kbytes : 0u);
+            if (++wu == KU && i + 1 < hi) {
+                wu = 0;
+                wb = weights(++wg);
+            }
+        };
+        // the tokens' values and the scales, one step ahead
+        const rsrc_t hb = buffer(h, (int64_t)s.T * s.k * s.I * 4);
+        const int KB = s.I / 128, HB = (s.H + 127) / 128;
+        rsrc_t sb;
+        int hg = wg, hu = wu, hrows = 0;
+        uint32_t hoff[RT];
+        const auto segment = [&](int g) {
+            hrows = seg[g].rows;
+#pragma unroll
+            for (int a = 0; a < RT; ++a) {
+                uint32_t q[4];   // one load for the wave, then the lane's choice
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_readfirstlane(seg[g].pair[4 * a + i]);
+                const uint32_t p01 = c8 & 2 ? q[1] : q[0], p23 = c8 & 2 ? q[3] : q[2];
+                const uint32_t two = c8 & 4 ? p23 : p01, pair = c8 & 1 ? two >> 16 : two & 0xFFFFu;
+                hoff[a] = 8 * a + c8 < hrows ? (pair * 2 + part) * (uint32_t)s.I * 2 : kPast;
+            }
+            if constexpr (F8) sb = buffer(downs + ((size_t)seg[g].expert * HB + n0 / 128) * KB, KB * 4);
+        };
+        segment(hg);
+        struct Values {
+            vec16 v[RT][C];
+            float scale;
+        };
+        const auto load_h = [&](int i, Values &to) {
+#pragma unroll
+            for (int a = 0; a < RT; ++a) {
+                if (a > 0 && hrows <= 8 * a) break;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const uint32_t at = (uint32_t)hu * (KE * 2) + S::at(c, quad);
+                    to.v[a][c] = load_16(hb, i < hi && at < (uint32_t)s.I * 2 ? hoff[a] + at : kPast, 0);
+                }
+            }
+            if constexpr (F8) to.scale = load_f32(sb, 0, (uint32_t)min(hu, KB - 1) * 4);
+        };
+
+        f32x4 sum[RT][G] = {};
+        int g = wg, u = wu, rows = hrows;
+        const uint32_t plo = (uint32_t)(r16 * 128 + ((quad ^ (r16 & 7)) << 4));
+        const auto finish = [&]() {   // the segment's sums to the tokens' lanes
+            const uint64_t tokens = seg[g].tokens;
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) sum[a][i][q] += __shfl_xor(sum[a][i][q], 8);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                if (((tokens >> (8 * t)) & 0xFF) == 0) continue;
+                const uint64_t bit = 1ull << (8 * t + c8);
+                const int r = __popcll(tokens & (bit - 1));
+                const bool in = (tokens & bit) != 0;
+#pragma unroll
+                for (int i = 0; i < G; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float v = __shfl(sum[0][i][q], quad * 16 + (r & 7));
+                        if constexpr (RT > 1) {
+                            const float v1 = __shfl(sum[1][i][q], quad * 16 + (r & 7));
+                            v = r < 8 ? v : v1;
+                        }
+                        acc[t][i][q] += in ? v : 0.0f;
+                    }
+            }
+#pragma unroll
+            for (int a = 0; a < RT; ++a)
+#pragma unroll
+                for (int i = 0; i < G; ++i) sum[a][i] = f32x4{};
+        };
+        const auto step = [&](uint8_t *buf, const Values &x, Values &next, int i) {
+            wait_step<NB, C + (F8 ? 1 : 0), 2 * G>(i - lo);
+            const uint8_t *p = buf + wid * (G * 2048);
+            const S wv(p, plo);
+            __builtin_amdgcn_sched_barrier(0);
+            if (++hu == KU && i + 1 < hi) {
+                hu = 0;
+                segment(++hg);
+            }
+            load_h(i + 1, next);
+            __builtin_amdgcn_sched_barrier(0);
+            stage(buf, i + NB);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int a = 0; a < RT; ++a) {
+                if (a > 0 && rows <= 8 * a) break;
+                f32x4 d[G];
+#pragma unroll
+                for (int f = 0; f < G; ++f) d[f] = F8 ? f32x4{} : sum[a][f];
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    const bf16x8 b = __builtin_bit_cast(bf16x8, x.v[a][c]);
+#pragma unroll
+                    for (int f = 0; f < G; ++f) d[f] = mfma(wv.a[f][c], b, d[f]);
+                }
+#pragma unroll
+                for (int f = 0; f < G; ++f)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        sum[a][f][q] = F8 ? __builtin_fmaf(d[f][q], x.scale, sum[a][f][q]) : d[f][q];
+            }
+            if (++u == KU || i + 1 == hi) {
+                finish();
+                u = 0;
+                ++g;
+                rows = hrows;   // the next step's segment
+            }
+        };
+        Values v[2];
+        stage(buf0, lo);
+        __builtin_amdgcn_sched_barrier(0);
+        load_h(lo, v[0]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 1; j < NB; ++j) stage(buf(j), lo + j);
+        constexpr int TURN = NB % 2 ? 2 * NB : NB;
+        for (int i = lo; i < hi; i += TURN) {
+#pragma unroll
+            for (int j = 0; j < TURN; ++j)
+                if (j == 0 || i + j < hi) step(buf(j), v[j % 2], v[(j + 1) % 2], i + j);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+    }
+
+    // add up the waves, in order
+    __syncthreads();
+    constexpr int TILE = NW * G * 32;   // f32x4 of 8 tokens: [wave][group of columns][quad][token]
+    static_assert((TT + 1) / 2 * TILE * 16 <= NW * G * 2048, "they fit in the first two buffers");
+    if (part == 0)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int f = 0; f < G; ++f)
+                reinterpret_cast<f32x4 *>(t & 1 ? buf1 : buf0)[(t >> 1) * TILE + (wid * G + f) * 32 + quad * 8 + c8] =
+                    acc[t][f];
+    __syncthreads();
+    for (int i = threadIdx.x; i < TT * G * 32; i += 64 * NW) {
+        const int at = i % (G * 32), t = i / (G * 32), token = 8 * t + at % 8, col = n0 + at / 8 * 4;
+        if (token >= s.T || col >= s.H) continue;   // H % 8 == 0
+        const f32x4 *sums = reinterpret_cast<const f32x4 *>(t & 1 ? buf1 : buf0) + (t >> 1) * TILE + at;
+        f32x4 v = {};
+#pragma unroll
+        for (int q = 0; q < NW; ++q) v += sums[q * G * 32];
+        const size_t o = (size_t)token * s.H + col;
+        if (residual) {
+            const uint2 r = *reinterpret_cast<const uint2 *>(residual + o);
+            v += f32x4{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
+        }
+        *reinterpret_cast<uint2 *>(y + o) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    }
+}
+
+template <bool F8, int RT, int TT>
+hipError_t launch_down(const FewShape &s, const int32_t *count, const FewSegment *seg, const uint16_t *h,
+                       const uint8_t *down, const float *downs, const uint16_t *residual, uint16_t *y,
+                       hipStream_t stream) {
+    constexpr int G = 2, NW = 8, NB = 4;
+    const int blocks = (s.H + 16 * G - 1) / (16 * G);
+    hipLaunchKernelGGL((ep_few_down_kernel<F8, RT, TT, G, NW, NB>), dim3((unsigned)blocks), dim3(64 * NW), 0, stream, s,
+                       count, seg, h, down, downs, residual, y);
+    return hipGetLastError();
+}
+
+template <bool F8>
+hipError_t launch(const FewShape &s, const uint16_t *x, const int64_t *idx, const float *w, const uint8_t *up,
+                  const float *ups, const uint8_t *down, const float *downs, const uint16_t *residual, uint16_t *y,
+                  uint8_t *ws, hipStream_t stream) {
+    int32_t *count = reinterpret_cast<int32_t *>(ws);
+    FewSegment *seg = reinterpret_cast<FewSegment *>(ws + kFewHead);
+    uint16_t *h = reinterpret_cast<uint16_t *>(ws + few_h_offset(s));
+    const int cols = (s.I + 15) / 16;
+    const dim3 grid((unsigned)(1 + (int64_t)s.T * s.k * cols));
+    if (s.T <= 16)
+        hipLaunchKernelGGL((ep_few_up_kernel<F8, 1, 4, 2>), grid, dim3(256), 0, stream, s, x, idx, w, up, ups, count, seg,
+                           h, cols);
+    else
+        hipLaunchKernelGGL((ep_few_up_kernel<F8, 2, 4, 3>), grid, dim3(256), 0, stream, s, x, idx, w, up, ups, count, seg,
+                           h, cols);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (s.T <= 8) return launch_down<F8, 1, 1>(s, count, seg, h, down, downs, residual, y, stream);
+    if (s.T <= 16) return launch_down<F8, 2, 2>(s, count, seg, h, down, downs, residual, y, stream);
+    if (s.T <= 32) return launch_down<F8, 2, 4>(s, count, seg, h, down, downs, residual, y, stream);
+    return launch_down<F8, 2, 8>(s, count, seg, h, down, downs, residual, y, stream);
+}
+
+}  // namespace
+
+hipError_t launch_few(const FewShape &s, const uint16_t *x, const int64_t *idx, const float *w, const void *up,
+                      const float *ups, const void *down, const float *downs, const uint16_t *residual, uint16_t *y,
+                      uint8_t *ws, hipStream_t stream) {
+    const uint8_t *u = static_cast<const uint8_t *>(up), *d = static_cast<const uint8_t *>(down);
+    return s.f8 ? launch<true>(s, x, idx, w, u, ups, d, downs, residual, y, ws, stream)
+                : launch<false>(s, x, idx, w, u, ups, d, downs, residual, y, ws, stream);
+}
+
+}  // namespace ep

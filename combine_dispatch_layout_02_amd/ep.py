@@ -38,6 +38,7 @@ EXPORTED = (
     "ep_expert_scale_bf16", "ep_expert_requant_mxfp8", "ep_expert_requant_nvfp4", "ep_accounting",
     "ep_calib_copy", "ep_stream", "ep_dispatch_with_layout_static", "ep_plan_info",
     "ep_route", "ep_route_backward", "ep_expert_gemm", "ep_expert_gated", "ep_combine_backward",
+    "ep_moe_few_workspace_bytes", "ep_moe_few", "ep_linear", "ep_linear_backward_workspace_bytes", "ep_linear_backward",
 )
 
 
@@ -94,6 +95,20 @@ class ep_expert_shape(ctypes.Structure):
         ("num_ranks", ctypes.c_int32),
         ("rank_capacity", ctypes.c_int32),
     ]
+
+
+EP_FEW_TOKENS = 64
+EP_ACT_NONE, EP_ACT_RELU, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_GELU_TANH = range(5)
+
+
+class ep_few_shape(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("num_tokens", "hidden", "intermediate", "num_experts", "num_topk",
+                                                    "w_format")]
+
+
+class ep_linear_shape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + [(name, ctypes.c_int32) for name in (
+        "in_features", "out_features", "activation", "gated", "y_f32", "grad_w_f32")]
 
 
 class ep_accounting_t(ctypes.Structure):
@@ -158,6 +173,7 @@ def load():
     lib = ctypes.CDLL(LIB_PATH)
     P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     SP, RP, XP = ctypes.POINTER(ep_shape), ctypes.POINTER(ep_router), ctypes.POINTER(ep_expert_shape)
+    FP, LP = ctypes.POINTER(ep_few_shape), ctypes.POINTER(ep_linear_shape)
     sig = {
         "ep_abi_version": (ctypes.c_int, []),
         "ep_strerror": (ctypes.c_char_p, [ctypes.c_int]),
@@ -190,6 +206,11 @@ def load():
         "ep_expert_gemm": (ctypes.c_int, [XP, P, P, P, P, P, P, P]),
         "ep_expert_gated": (ctypes.c_int, [XP, P, P, P, P, P, P, P, P]),
         "ep_combine_backward": (ctypes.c_int, [SP, P, P, P, P, P, P, P]),
+        "ep_moe_few_workspace_bytes": (ctypes.c_int, [FP, ctypes.POINTER(sz)]),
+        "ep_moe_few": (ctypes.c_int, [FP] + [P] * 9 + [P, sz, P]),
+        "ep_linear": (ctypes.c_int, [LP] + [P] * 6 + [P]),
+        "ep_linear_backward_workspace_bytes": (ctypes.c_int, [LP, ctypes.POINTER(sz)]),
+        "ep_linear_backward": (ctypes.c_int, [LP] + [P] * 7 + [P, sz, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -690,6 +711,115 @@ def ep_combine_backward(shape, dy, expert_out, token_slot, topk_w, grad_expert_o
     _ok(load().ep_combine_backward(ctypes.byref(shape), *args), "ep_combine_backward")
 
 
+# --------------------------------------------------------------------------- a few tokens, dense products
+
+_ACTIVATIONS = {None: EP_ACT_NONE, "relu": EP_ACT_RELU, "silu": EP_ACT_SILU, "gelu": EP_ACT_GELU,
+                "gelu_tanh": EP_ACT_GELU_TANH}
+
+
+def _few_shape(x, topk_idx, gate_up, gate_up_scales, down, down_scales) -> ep_few_shape:
+    if x.dim() != 2 or topk_idx.dim() != 2 or gate_up.dim() != 3 or gate_up.shape[1] % 2:
+        raise ValueError("expected x (T, H), topk_idx (T, k), gate_up (E, 2 I, H)")
+    (T, H), k, E, I = x.shape, topk_idx.shape[1], gate_up.shape[0], gate_up.shape[1] // 2   # noqa: E741
+    fp8 = gate_up_scales is not None
+    _need(x, torch.bfloat16, (T, H), "x")
+    _need(topk_idx, torch.int64, (T, k), "topk_idx")
+    dtype = torch.uint8 if fp8 else torch.bfloat16
+    _need(gate_up, dtype, (E, 2 * I, H), "gate_up")
+    _need(down, dtype, (E, H, I), "down")
+    if (down_scales is not None) != fp8:
+        raise ValueError("expected scales of gate_up and of down (e4m3 weights), or of neither (bf16)")
+    if fp8:
+        if H % 128 or I % 128:
+            raise ValueError("e4m3 weights: expected H and I multiples of 128")
+        _need(gate_up_scales, torch.float32, (E, 2 * I // 128, H // 128), "gate_up_scales")
+        _need(down_scales, torch.float32, (E, H // 128, I // 128), "down_scales")
+    return ep_few_shape(T, H, I, E, k, EP_FMT_FP8_S128 if fp8 else EP_FMT_BF16)
+
+
+def moe_few_workspace_bytes(T, H, I, E, k, w_format=EP_FMT_FP8_S128) -> int:   # noqa: E741
+    """Bytes of the workspace ep_moe_few takes."""
+    sh, n = ep_few_shape(int(T), int(H), int(I), int(E), int(k), int(w_format)), ctypes.c_size_t()
+    _ok(load().ep_moe_few_workspace_bytes(ctypes.byref(sh), ctypes.byref(n)), "ep_moe_few_workspace_bytes")
+    return n.value
+
+
+def ep_moe_few(x, topk_idx, topk_w, gate_up, gate_up_scales, down, down_scales, residual, y, ws, stream=None):
+    """The experts' layer for up to EP_FEW_TOKENS tokens: e4m3 weights with
+    their block scales, or bf16 weights and None; ws: a uint8 tensor."""
+    sh = _few_shape(x, topk_idx, gate_up, gate_up_scales, down, down_scales)
+    _need(topk_w, torch.float32, topk_idx.shape, "topk_w")
+    if residual is not None:
+        _need(residual, torch.bfloat16, x.shape, "residual")
+    _need(y, torch.bfloat16, x.shape, "y")
+    _need(ws, torch.uint8, (ws.numel(),), "ws")
+    *args, raw = _here(stream, x, topk_idx, topk_w, gate_up, gate_up_scales, down, down_scales, residual, y, ws)
+    _ok(load().ep_moe_few(ctypes.byref(sh), *args, ws.numel(), raw), "ep_moe_few")
+
+
+def _linear_shape(x, w, activation, gated, y_dtype, grad_w_dtype=torch.bfloat16) -> ep_linear_shape:
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation: expected one of {list(_ACTIVATIONS)}, got {activation!r}")
+    for dtype, name in ((y_dtype, "y"), (grad_w_dtype, "grad_w")):
+        if dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError(f"{name}: expected float32 or bfloat16, got {dtype}")
+    if x.dim() != 2 or w.dim() != 2 or (gated and w.shape[0] % 2):
+        raise ValueError("expected x (M, K), w (N, K), with a gate (2 N, K)")
+    (M, K), wide = x.shape, w.shape[0]
+    _need(x, torch.bfloat16, (M, K), "x")
+    _need(w, torch.bfloat16, (wide, K), "w")
+    return ep_linear_shape(M, K, wide // 2 if gated else wide, _ACTIVATIONS[activation], int(bool(gated)),
+                           int(y_dtype == torch.float32), int(grad_w_dtype == torch.float32))
+
+
+def ep_linear(x, w, bias, residual, y, z=None, activation=None, gated=False, stream=None):
+    """y = act(x w^T + bias) + residual, gated: act(first half) * second half;
+    z (or None) keeps x w^T + bias for the backward pass."""
+    sh = _linear_shape(x, w, activation, gated, y.dtype)
+    M, N, wide = x.shape[0], sh.out_features, w.shape[0]
+    if bias is not None:
+        _need(bias, torch.float32, (wide,), "bias")
+    if residual is not None:
+        _need(residual, torch.bfloat16, (M, N), "residual")
+    _need(y, y.dtype, (M, N), "y")
+    if z is not None:
+        _need(z, torch.bfloat16, (M, wide), "z")
+    args = _here(stream, x, w, bias, residual, y, z)
+    _ok(load().ep_linear(ctypes.byref(sh), *args), "ep_linear")
+
+
+def linear_backward_workspace_bytes(M, K, N, activation=None, gated=False, y_dtype=torch.bfloat16,
+                                    grad_w_dtype=torch.bfloat16) -> int:
+    """Bytes of the workspace ep_linear_backward takes."""
+    sh = ep_linear_shape(int(M), int(K), int(N), _ACTIVATIONS[activation], int(bool(gated)),
+                         int(y_dtype == torch.float32), int(grad_w_dtype == torch.float32))
+    n = ctypes.c_size_t()
+    _ok(load().ep_linear_backward_workspace_bytes(ctypes.byref(sh), ctypes.byref(n)),
+        "ep_linear_backward_workspace_bytes")
+    return n.value
+
+
+def ep_linear_backward(dy, x, w, z, grad_x, grad_w, grad_bias, ws, activation=None, gated=False, stream=None):
+    """Gradients of ep_linear from dy and the z it kept (None where there is
+    neither activation nor gate); those that are None are not computed."""
+    sh = _linear_shape(x, w, activation, gated, dy.dtype, torch.bfloat16 if grad_w is None else grad_w.dtype)
+    M, N, wide = x.shape[0], sh.out_features, w.shape[0]
+    _need(dy, dy.dtype, (M, N), "dy")
+    if activation is not None or gated:
+        if z is None:
+            raise ValueError("z: needed where there is an activation or a gate")
+        _need(z, torch.bfloat16, (M, wide), "z")
+    if grad_x is not None:
+        _need(grad_x, torch.bfloat16, x.shape, "grad_x")
+    if grad_w is not None:
+        _need(grad_w, grad_w.dtype, w.shape, "grad_w")
+    if grad_bias is not None:
+        _need(grad_bias, torch.float32, (wide,), "grad_bias")
+    _need(ws, torch.uint8, (ws.numel(),), "ws")
+    *args, raw = _here(stream, dy, x, w, z, grad_x, grad_w, grad_bias, ws)
+    _ok(load().ep_linear_backward(ctypes.byref(sh), *args, ws.numel(), raw), "ep_linear_backward")
+
+
 def ep_accounting(shape, own_node, num_tokens_per_rank, num_tokens_per_node, rdma_algo_token_count,
                   valid_pairs) -> dict:
     """Host arithmetic on host copies of the counts (numpy int32 arrays)."""
@@ -931,3 +1061,44 @@ def combine_backward(dy, expert_out, handle: Handle, stream=None):
     g, gw = _alloc(expert_out, (expert_out.shape, torch.bfloat16), (handle.topk_w.shape, torch.float32), stream=stream)
     ep_combine_backward(handle.shape, dy, expert_out, handle.token_slot, handle.topk_w, g, gw, stream)
     return g, gw
+
+
+# --------------------------------------------------------------------------- a few tokens, dense products (allocating)
+
+def moe_few(x, topk_idx, topk_w, gate_up, down, gate_up_scales=None, down_scales=None, residual=None, ws=None,
+            stream=None):
+    """y [T, H] bf16 of the experts' layer for a few tokens; ws: the caller's workspace, or allocated."""
+    if ws is None:
+        sh = _few_shape(x, topk_idx, gate_up, gate_up_scales, down, down_scales)
+        n = ctypes.c_size_t()
+        _ok(load().ep_moe_few_workspace_bytes(ctypes.byref(sh), ctypes.byref(n)), "ep_moe_few_workspace_bytes")
+        y, ws = _alloc(x, (x.shape, torch.bfloat16), (n.value, torch.uint8), stream=stream)
+    else:
+        y, = _alloc(x, (x.shape, torch.bfloat16), stream=stream)
+    ep_moe_few(x, topk_idx, topk_w, gate_up, gate_up_scales, down, down_scales, residual, y, ws, stream)
+    return y
+
+
+def linear(x, w, bias=None, residual=None, activation=None, gated=False, out_dtype=torch.bfloat16, save=False,
+           stream=None):
+    """y [M, N], or y and z with `save`."""
+    M, wide = x.shape[0], w.shape[0]
+    y, = _alloc(x, ((M, wide // 2 if gated else wide), out_dtype), stream=stream)
+    z = _alloc(x, ((M, wide), torch.bfloat16), stream=stream)[0] if save else None
+    ep_linear(x, w, bias, residual, y, z, activation, gated, stream)
+    return (y, z) if save else y
+
+
+def linear_backward(dy, x, w, z=None, activation=None, gated=False, bias=False, grad_w_dtype=torch.bfloat16, ws=None,
+                    stream=None):
+    """Returns grad_x [M, K] bf16 and grad_w like w, with `bias` grad_bias [N or 2 N] fp32 too."""
+    sh = _linear_shape(x, w, activation, gated, dy.dtype, grad_w_dtype)
+    if ws is None:
+        n = ctypes.c_size_t()
+        _ok(load().ep_linear_backward_workspace_bytes(ctypes.byref(sh), ctypes.byref(n)),
+            "ep_linear_backward_workspace_bytes")
+        ws, = _alloc(x, (n.value, torch.uint8), stream=stream)
+    gx, gw = _alloc(x, (x.shape, torch.bfloat16), (w.shape, grad_w_dtype), stream=stream)
+    gb = _alloc(x, (w.shape[0], torch.float32), stream=stream)[0] if bias else None
+    ep_linear_backward(dy, x, w, z, gx, gw, gb, ws, activation, gated, stream)
+    return (gx, gw, gb) if bias else (gx, gw)

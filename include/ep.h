@@ -598,6 +598,123 @@ int ep_combine_backward(const ep_shape *shape, const uint16_t *dy, const uint16_
                         const int32_t *token_slot, const float *topk_w, uint16_t *grad_expert_out,
                         float *grad_topk_w, void *stream);
 
+/* ---- the experts' layer for a few tokens -------------------------------------- */
+
+/* Supported range (else EP_EINVAL): 0 <= num_tokens <= EP_FEW_TOKENS; 1 <=
+ * num_experts <= 4096; 1 <= num_topk <= 32; w_format EP_FMT_BF16 with hidden
+ * and intermediate multiples of 8, or EP_FMT_FP8_S128 with both multiples of
+ * 128; both at least 8 and at most 2^20; num_tokens * num_topk * intermediate <
+ * 2^28 (the launch grid). */
+#define EP_FEW_TOKENS 64
+typedef struct ep_few_shape {
+    int32_t num_tokens;    /* T */
+    int32_t hidden;        /* H: width of x and y */
+    int32_t intermediate;  /* I: width of an expert's gated product */
+    int32_t num_experts;   /* E */
+    int32_t num_topk;      /* k */
+    int32_t w_format;      /* of the weights: EP_FMT_BF16 | EP_FMT_FP8_S128 */
+} ep_few_shape;
+
+/* Host-only: bytes of device workspace ep_moe_few needs. */
+int ep_moe_few_workspace_bytes(const ep_few_shape *shape, size_t *bytes);
+
+/*
+ * The whole layer of experts for a few tokens (decoding), from the router's
+ * choice to the tokens' results, in two launches and without a dispatch: the
+ * experts' weights are read once each, and the tokens' rows stay where they are.
+ *     g = G_e x[t], u = U_e x[t]          e = topk_idx[t, j]
+ *     y[t] = bf16_rne(residual[t] + sum_j D_e (topk_w[t, j] * (silu(g) * u)))
+ * x enters as it is, in bf16; products and sums are fp32 (16-bit matrix
+ * instructions; e4m3 weights are widened exactly and their sums scaled per 128
+ * x 128 block); the gated product, times its weight, is carried from the first
+ * launch to the second as two bf16 parts, 2^-17 of it lost; one rounding at the
+ * end.  (Where a bf16 weight of D is infinite the result can be NaN instead of
+ * infinite, the second part being 0.)  Deterministic.
+ *   - A negative id, or one >= num_experts, is a masked slot: it adds nothing,
+ *     and its weight is not looked at.  A token whose slots are all masked gets
+ *     its residual, or +0.
+ *   - An expert that a token names twice counts twice (its weights are added).
+ *   - Experts that no token names are not read.
+ *   x         [T, H] bf16; topk_idx [T, k] int64; topk_w [T, k] fp32: as ep_route gives them
+ *   gate_up   [E, 2 I, H]: I gate rows (G), then I up rows (U); e4m3 with
+ *             gate_up_scales [E, 2 I / 128, H / 128] fp32, or bf16 and NULL
+ *   down      [E, H, I] (D); e4m3 with down_scales [E, H / 128, I / 128], or bf16 and NULL
+ *             (the weights of ep_expert_gated and ep_expert_gemm)
+ *   residual  [T, H] bf16 or NULL
+ *   y         [T, H] bf16; it may be x's or residual's buffer and overlaps no other input
+ *   ws        ep_moe_few_workspace_bytes, 256-byte aligned; it needs no clearing
+ *             and holds nothing from one call to the next
+ * x, gate_up, down, residual and y are 16-byte aligned.
+ */
+int ep_moe_few(const ep_few_shape *shape, const uint16_t *x, const int64_t *topk_idx, const float *topk_w,
+               const void *gate_up, const float *gate_up_scales, const void *down, const float *down_scales,
+               const uint16_t *residual, uint16_t *y, void *ws, size_t ws_bytes, void *stream);
+
+/* ---- the matrix product with bias, activation and residual ---------------------- */
+
+enum ep_activation {
+    EP_ACT_NONE = 0,
+    EP_ACT_RELU = 1,        /* max(z, 0) */
+    EP_ACT_SILU = 2,        /* z / (1 + exp(-z)) */
+    EP_ACT_GELU = 3,        /* z erfc(-z / sqrt(2)) / 2 */
+    EP_ACT_GELU_TANH = 4    /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+};
+
+/* Supported range (else EP_EINVAL): rows >= 0; in_features and out_features
+ * multiples of 8, from 8 to 2^20; the launch grids' limits: of rows / 64 + 1,
+ * in_features / 64 + 1 and wide / 64 + 1 (wide = out_features, twice that where
+ * gated) the product of any two is below 2^23. */
+typedef struct ep_linear_shape {
+    int64_t rows;           /* M */
+    int32_t in_features;    /* K */
+    int32_t out_features;   /* N: width of y */
+    int32_t activation;     /* EP_ACT_* */
+    int32_t gated;          /* 1: w has 2 N rows, N that are activated, then N that multiply them */
+    int32_t y_f32;          /* 1: y (and its gradient) is fp32, 0: bf16 */
+    int32_t grad_w_f32;     /* 1: the weights' gradient is fp32, 0: bf16 (backward only) */
+} ep_linear_shape;
+
+/*
+ * The dense products of the layer: the router's logits, a shared expert whose
+ * result joins the combine's.
+ *     z = x w^T + bias               [M, N], gated: [M, 2 N]
+ *     y = act(z) + residual          gated: act(z[:, :N]) * z[:, N:] + residual
+ * with fp32 accumulation (16-bit matrix instructions) and an fp32 epilogue;
+ * rounded once.  Deterministic for a shape.
+ *   x [M, K] bf16; w [N or 2 N, K] bf16; bias [N or 2 N] fp32 or NULL
+ *   residual [M, N] bf16 or NULL
+ *   y        [M, N] bf16 or fp32; it may be residual's buffer (bf16) and overlaps no other input
+ *   z        [M, N or 2 N] bf16 or NULL: what the backward pass needs where
+ *            there is an activation or a gate (y is computed from the fp32 values)
+ * x, w, bias, residual, y and z are 16-byte aligned.
+ */
+int ep_linear(const ep_linear_shape *shape, const uint16_t *x, const uint16_t *w, const float *bias,
+              const uint16_t *residual, void *y, uint16_t *z, void *stream);
+
+/* Host-only: bytes of device workspace ep_linear_backward needs. */
+int ep_linear_backward_workspace_bytes(const ep_linear_shape *shape, size_t *bytes);
+
+/*
+ * Gradients of ep_linear from the gradient dy of its result and the z it kept:
+ *     dz = dy * act'(z)     gated: [dy * z[:, N:] * act'(z[:, :N]), dy * act(z[:, :N])]
+ *     grad_x = dz w, grad_w = dz^T x, grad_bias = sum over rows of dz
+ * (that of the residual is dy itself; relu' is 0 at 0).  dz is computed in fp32.  For the two
+ * products it is rounded to bf16, half a step of which is what the rounding of
+ * their bf16 results is; for an fp32 grad_w it enters as two bf16 parts (2^-17
+ * lost) unless it is dy itself.  grad_bias is the sum of the fp32 values, in fp32, in a fixed
+ * order.  Deterministic for a shape.
+ *   dy [M, N] bf16 or fp32 (y_f32); z [M, N or 2 N] bf16, NULL where there is
+ *   neither activation nor gate; x, w as for ep_linear
+ *   grad_x [M, K] bf16, grad_w [N or 2 N, K] bf16 or fp32 (grad_w_f32),
+ *   grad_bias [N or 2 N] fp32: each may be NULL, and is then not computed; they overlap no input
+ *   With no rows, grad_w and grad_bias are 0.
+ *   ws 256-byte aligned; it needs no clearing and holds nothing from one call to the next
+ * dy, z, x, w, grad_x and grad_w are 16-byte aligned.
+ */
+int ep_linear_backward(const ep_linear_shape *shape, const void *dy, const uint16_t *x, const uint16_t *w,
+                       const uint16_t *z, uint16_t *grad_x, void *grad_w, float *grad_bias, void *ws,
+                       size_t ws_bytes, void *stream);
+
 /* ---- accounting (host arithmetic on host copies of the layout counts) ---- */
 
 /* [MORI] "Bandwidth Computation": RDMA algo tokens are the layout's (token,
