@@ -54,11 +54,11 @@ struct LinearShape {
     bool plain() const { return act == kActNone && !gated && !f32; }
 };
 
-// Workspace of the backward pass: dz in bf16 (twice, as two parts, for an fp32
+// Workspace of the backward pass: dz in bf16 (in three parts for an fp32
 // gradient of the weights) unless it is dy itself, the bias' sums of runs of rows.
-constexpr int kDzRows = 64;   // rows of a run
+constexpr int kDzRows = 32;   // rows of a run
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-inline int dz_parts(const LinearShape &s) { return s.plain() ? 0 : (s.w32 ? 2 : 1); }
+inline int dz_parts(const LinearShape &s) { return s.plain() ? 0 : (s.w32 ? 3 : 1); }
 inline size_t linear_sums_offset(const LinearShape &s) {
     return align256((size_t)dz_parts(s) * s.M * s.wide() * 2);
 }

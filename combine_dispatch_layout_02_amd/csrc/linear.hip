@@ -101,7 +101,7 @@ struct Operand {
 struct Product {
     Operand r, q;
     int64_t k;         // length of the sums
-    int64_t part;      // elements from dz's first part to its second (parts 2)
+    int64_t part;      // elements from one part of dz to the next
     int parts;         // the sums run over k as often, R from its parts in turn
     int rtiles, ctiles;
     // what becomes of the sums
@@ -115,121 +115,169 @@ struct Product {
     bool gated, linear;   // linear: bias, activation, ... follow
 };
 
-// The lane's part in bringing B rows of an operand into LDS, NL loads of 1 KiB
-// by each of W waves.
-//   k contiguous (T false): LDS rows are operand rows of 64 k, 128 bytes; piece
-//     c of 16 bytes lies at c ^ (row % 8), so that 8 rows' pieces touch every
-//     bank once.
-//   rows contiguous (T true): LDS rows are k, 2 B bytes; pairs of pieces are
-//     permuted by k % 4: the transposing read takes 32 bytes of 4 consecutive k.
-template <bool T, int B, int W>
-struct Loader {
-    static constexpr int NL = B * 128 / 1024 / W;
-    static_assert(NL >= 1 && NL * W * 1024 == B * 128, "whole loads");
+// The lane's part in bringing B rows by KS of k of an operand into LDS, NL loads
+// of 1 KiB by each of W waves, and in reading it from there.
+//   k contiguous (T false): LDS rows are operand rows, 128 (KS = 64) or 64 bytes.
+//     Their 16-byte pieces are permuted by the row (`place`), so that the 16
+//     lanes that one cycle of a 16-byte LDS read serves (0-3, 12-15, 20-27, and
+//     the others of 32) touch every bank once.
+//   rows contiguous (T true): LDS rows are lines of k, 2 B bytes.  The transposing
+//     read takes 32 bytes of 4 lines for 16 lanes, and of 8 lines for 32: those go
+//     to 8 different loads (`line`), whose places lie 32 bytes off each other.
+template <bool T, int B, int W, int KS>
+struct Side {
+    static constexpr int NL = B * KS * 2 / 1024 / W, BLOCKS = NL * W, PIECES = KS / 8;
+    static_assert(NL >= 1 && BLOCKS * 1024 == B * KS * 2, "whole loads");
+    static constexpr int LINE = 2 * B, PLACE = T ? 1056 : 1024, BYTES = BLOCKS * PLACE;
     const uint16_t *base;
-    int64_t step;         // elements from one step to the next (T: a step's 64 lines)
+    int64_t step;         // elements from one step to the next (T: a step's KS lines)
     int64_t second;       // elements to the second half of a gated tile
     uint32_t off[NL];
     int kfirst[T ? NL : 1];   // T: the line; else the lane's first k in a step
-    __device__ __forceinline__ void init(const Operand &o, int64_t first, int lane, int wid) {
+    uint32_t from;            // the lane's part of a fragment's place in LDS
+
+    static __device__ __forceinline__ int place(int row) { return KS == 64 ? row & 7 : (4 - (row >> 2)) & 3; }
+    // The line in place s (s % BLOCKS: the load, s / BLOCKS: where in it): 0-3, 8-11, 4-7, 12-15, 16-19, ...
+    static __device__ __forceinline__ int line(int s) { return (s & 0x33) | (s & 4) << 1 | (s & 8) >> 1; }
+    static constexpr int line_at(int s) { return s % BLOCKS * PLACE + s / BLOCKS * LINE; }
+
+    // first: the tile's first row, row: the wave's first row in the tile
+    __device__ __forceinline__ void init(const Operand &o, int64_t first, int row, int lane, int wid) {
+        const int r16 = lane & 15, quad = lane >> 4;
         if constexpr (!T) {
             base = o.p + first * o.ld;
-            step = 64;
+            step = KS;
             second = o.split * o.ld;
-            const int row = lane >> 3, piece = (lane & 7) ^ row;
+            const int lr = lane / PIECES, piece = (lane % PIECES) ^ place(lr);
             kfirst[0] = piece * 8;
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
-                const int at = (wid * NL + i) * 8 + row;   // LDS row; those past the end repeat the last one
+                const int at = (wid * NL + i) * (64 / PIECES) + lr;   // LDS row; those past the end repeat the last one
                 const int r = o.split > 0 && at >= B / 2 ? at - B / 2 : at;
                 const int64_t last = (o.split > 0 ? o.split : o.rows) - 1 - first;
                 off[i] = (uint32_t)(min((int64_t)r, last) * o.ld * 2) + piece * 16;
             }
+            from = (uint32_t)((row + r16) * (KS * 2) + ((quad ^ place(r16)) << 4));
         } else {
             base = o.p + first;
-            step = 64 * o.ld;
+            step = KS * o.ld;
             second = 0;
             const int last = (int)min((o.rows - first) / 8 - 1, (int64_t)(B / 8 - 1));   // pieces of a line
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
-                const int at = (wid * NL + i) * 64 + lane, line = at / (B / 8), slot = at % (B / 8);
-                const int piece = min(slot ^ ((line & 3) << 1), last);
-                kfirst[i] = line;
-                off[i] = (uint32_t)(line * o.ld * 2) + piece * 16;
+                kfirst[i] = line(wid * NL + i + lane * 16 / LINE * BLOCKS);
+                off[i] = (uint32_t)(kfirst[i] * o.ld * 2) + min(lane * 16 % LINE / 16, last) * 16;
             }
+            // lane i of 16 names line i / 4 and its columns 4 (i % 4) .. + 3, and gets column i of the 4 lines
+            from = (uint32_t)(((r16 >> 2) + 4 * (quad & 1)) * PLACE + (quad >> 1) * line_at(16) + (row + (r16 & 3) * 4) * 2);
         }
     }
     // from: the step's first element, left: of the sum's length from there on
-    __device__ __forceinline__ void load(uint8_t *lds, int i, int wid, const uint16_t *from, int left) const {
-        const rsrc_t b = buffer(!T && (wid * NL + i) * 8 >= B / 2 ? from + second : from);
+    __device__ __forceinline__ void load(uint8_t *lds, int i, int wid, const uint16_t *p, int left) const {
+        const rsrc_t b = buffer(!T && (wid * NL + i) * (64 / PIECES) >= B / 2 ? p + second : p);
         const uint32_t past = kfirst[T ? i : 0] < left ? 0u : kPast;
-        load_to_lds(b, lds + (wid * NL + i) * 1024, off[i] | past, 0);
+        load_to_lds(b, lds + (wid * NL + i) * PLACE, off[i] | past, 0);
+    }
+    // 16 rows (the wave's first + row) by 32 k in the matrix instruction's layout: lane (l % 16: row, l / 16: 8 of k)
+    __device__ __forceinline__ bf16x8 fragment(const uint8_t *lds, int row, int chunk) const {
+        if constexpr (!T) {
+            // 4 pieces on is a change of one bit of the permuted place
+            return __builtin_bit_cast(bf16x8, ld16(lds + (chunk ? from ^ 64 : from) + row * (KS * 2)));
+        } else {
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            const uint8_t *p = lds + from + row * 2 + line_at(32 * chunk);
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + line_at(8)));
+            return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+        }
     }
 };
 
-// A fragment of 16 rows by 32 k of an operand in LDS, in the matrix
-// instruction's layout: lane (l % 16: row, l / 16: 8 consecutive k).
-template <bool T, int B>
-__device__ __forceinline__ bf16x8 fragment(const uint8_t *lds, int row, int chunk, int lane) {
-    const int r16 = lane & 15, quad = lane >> 4;
-    if constexpr (!T) {
-        const int r = row + r16;
-        return __builtin_bit_cast(bf16x8, ld16(lds + r * 128 + (((chunk * 4 + quad) ^ (r & 7)) << 4)));
-    } else {
-        typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-        const int k = chunk * 32 + quad * 8 + (r16 >> 2);
-        // lane i of 16 names line i / 4 and its columns 4 (i % 4) .. + 3, and gets column i of the 4 lines
-        const int col = row + (r16 & 3) * 4, piece = (col >> 3) ^ ((r16 >> 2) << 1);
-        const uint8_t *p = lds + k * (2 * B) + piece * 16 + (col & 7) * 2;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * 2 * B));
-        return __builtin_bit_cast(bf16x8, s16x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]});
+// 8 results of a row, as a lane has them for the epilogue.
+struct Eight {
+    float v[8];
+    // The lane's 4 values of one group of 16 columns (at 4 quad) and of the next
+    // become 8 neighbours of one of them: lanes of odd quads hand over their a
+    // for the b of the quad before.  A store is then 16 bytes a lane, 64 a row.
+    __device__ __forceinline__ Eight(const f32x4 &a, const f32x4 &b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const auto s = __builtin_amdgcn_permlane16_swap(f2u(a[i]), f2u(b[i]), false, false);
+            v[i] = u2f(s[0]);
+            v[4 + i] = u2f(s[1]);
+        }
     }
-}
+    // The first of those columns, from the first of a's group.
+    static __device__ __forceinline__ int column(int quad) { return 16 * (quad & 1) + 8 * (quad >> 1); }
+    __device__ __forceinline__ void add(const float *p) {   // 8 fp32 values
+        const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] += a[i], v[4 + i] += b[i];
+    }
+    __device__ __forceinline__ void add(vec16 w) {   // 8 bf16 values
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[2 * i] += bf16_lo(w[i]), v[2 * i + 1] += bf16_hi(w[i]);
+    }
+    __device__ __forceinline__ void store(float *p) const {
+        *reinterpret_cast<f32x4 *>(p) = f32x4{v[0], v[1], v[2], v[3]};
+        *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    }
+    __device__ __forceinline__ void store(uint16_t *p) const {
+        st16(p, vec16{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                      pack_bf16x2(v[6], v[7])});
+    }
+    __device__ __forceinline__ void store(void *out, bool f32, int64_t at) const {
+        if (f32)
+            store(static_cast<float *>(out) + at);
+        else
+            store(static_cast<uint16_t *>(out) + at);
+    }
+};
 
-__device__ __forceinline__ void store4(void *out, bool f32, int64_t at, const f32x4 &v) {
-    if (f32)
-        *reinterpret_cast<f32x4 *>(static_cast<float *>(out) + at) = v;
-    else
-        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + at) =
-            uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-}
-
-// The last steps of 4 results at row r and columns c .. c + 3 (gated: the gate's
-// in v, the factor's in u).
-__device__ __forceinline__ void finish4(const Product &p, int64_t r, int64_t c, f32x4 v, f32x4 u) {
+// The last steps of 8 results at row r, columns c .. c + 7 (gated: their factors in u).
+__device__ __forceinline__ void finish(const Product &p, int64_t r, int64_t c, Eight v, Eight u, vec16 residual) {
     const int64_t at = r * p.out_ld + c;
     if (p.linear) {
         if (p.bias) {
-            v += *reinterpret_cast<const f32x4 *>(p.bias + c);
-            if (p.gated) u += *reinterpret_cast<const f32x4 *>(p.bias + p.out_ld + c);
+            v.add(p.bias + c);
+            if (p.gated) u.add(p.bias + p.out_ld + c);
         }
         if (p.z) {
-            store4(p.z, false, p.gated ? r * 2 * p.out_ld + c : at, v);
-            if (p.gated) store4(p.z, false, r * 2 * p.out_ld + p.out_ld + c, u);
+            v.store(p.z + (p.gated ? at + r * p.out_ld : at));
+            if (p.gated) u.store(p.z + at + (r + 1) * p.out_ld);
         }
         with_activation(p.act, [&](auto act) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = activate<decltype(act)::value>(v[i]);
+            for (int i = 0; i < 8; ++i) v.v[i] = activate<decltype(act)::value>(v.v[i]);
         });
-        if (p.gated) v *= u;
-        if (p.residual) {
-            const uint2 d = *reinterpret_cast<const uint2 *>(p.residual + at);
-            v += f32x4{bf16_lo(d.x), bf16_hi(d.x), bf16_lo(d.y), bf16_hi(d.y)};
-        }
+        if (p.gated)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v.v[i] *= u.v[i];
+        if (p.residual) v.add(residual);
     }
-    store4(p.out, p.out_f32, at, v);
+    v.store(p.out, p.out_f32, at);
 }
 
-// One block: BR rows by BC columns of C, WR by WC waves; a step is 64 of k.
-template <bool TR, bool TQ, int BR, int BC, int WR, int WC>
+// One block: BR rows by BC columns of C, WR by WC waves; a step is KS of k. NB
+// steps' operands have room in LDS: while step s is multiplied, the fragments of
+// s + 1 are read and the operands of s + NB are on their way into the place of s,
+// which every wave had read before the barrier.
+template <bool TR, bool TQ, int BR, int BC, int WR, int WC, int KS, int NB>
 __global__ __launch_bounds__(64 * WR * WC) void ep_linear_tile_kernel(Product p) {
-    constexpr int W = WR * WC, NR = BR / WR / 16, NC = BC / WC / 16;
-    static_assert(NC % 2 == 0, "a gate's columns and their factors in one wave");
-    __shared__ __attribute__((aligned(16))) uint8_t rbuf0[BR * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t qbuf0[BC * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t rbuf1[BR * 128];
-    __shared__ __attribute__((aligned(16))) uint8_t qbuf1[BC * 128];
+    constexpr int W = WR * WC, NR = BR / WR / 16, NC = BC / WC / 16, CH = KS / 32;
+    typedef Side<TR, BR, W, KS> R;
+    typedef Side<TQ, BC, W, KS> Q;
+    constexpr int BYTES = R::BYTES + Q::BYTES;
+    static_assert(NC % 4 == 0, "pairs of groups of a gate's columns and of their factors in one wave");
+    static_assert(NB >= 3 && NB <= 5, "as many buffers");
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t buf3[NB > 3 ? BYTES : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t buf4[NB > 4 ? BYTES : 16];
+    const auto buf = [&](int j) {
+        return j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : (j % NB == 2 ? buf2 : (j % NB == 3 ? buf3 : buf4)));
+    };
 
     int rt, ct;
     if (!TileOrder{p.rtiles, p.ctiles}.tile(blockIdx.x, &rt, &ct)) return;
@@ -237,163 +285,360 @@ __global__ __launch_bounds__(64 * WR * WC) void ep_linear_tile_kernel(Product p)
     const int wr = wid / WC, wc = wid % WC;
     const int64_t r0 = (int64_t)rt * BR, c0 = (int64_t)ct * (p.gated ? BC / 2 : BC);
 
-    Loader<TR, BR, W> lr;
-    Loader<TQ, BC, W> lq;
-    lr.init(p.r, r0, lane, wid);
-    lq.init(p.q, c0, lane, wid);
-    const int steps = (int)((p.k + 63) / 64), all = steps * p.parts;
-    const auto stage = [&](uint8_t *rb, uint8_t *qb, int s) {
-        const int part = s >= steps ? 1 : 0, kb = s - part * steps;
-        const int left = s < all ? (int)min(p.k - (int64_t)kb * 64, (int64_t)64) : 0;
-        const uint16_t *rp = lr.base + part * p.part + kb * lr.step, *qp = lq.base + kb * lq.step;
-#pragma unroll
-        for (int i = 0; i < lr.NL; ++i) lr.load(rb, i, wid, rp, left);
-#pragma unroll
-        for (int i = 0; i < lq.NL; ++i) lq.load(qb, i, wid, qp, left);
-    };
-    // LDS rows of the wave's groups of 16 columns: half of them from each half of the tile
-    const auto qrow = [&](int f) { return (f / (NC / 2)) * (BC / 2) + wc * (BC / 2 / WC) + f % (NC / 2) * 16; };
-
-    f32x4 acc[NC][NR] = {};
-    const auto step = [&](const uint8_t *rb, const uint8_t *qb, uint8_t *rnext, uint8_t *qnext, int s) {
-        // this wave's part of the step has arrived; then every wave's, and the other buffers are free
-        wait_loads<0>();
-        barrier_only();
-        stage(rnext, qnext, s + 1);
-        __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            bf16x8 b[NR];
-#pragma unroll
-            for (int m = 0; m < NR; ++m) b[m] = fragment<TR, BR>(rb, wr * (BR / WR) + 16 * m, c, lane);
-#pragma unroll
-            for (int f = 0; f < NC; ++f) {
-                const bf16x8 a = fragment<TQ, BC>(qb, qrow(f), c, lane);
-#pragma unroll
-                for (int m = 0; m < NR; ++m) acc[f][m] = mfma(a, b[m], acc[f][m]);
-            }
+    // the wave's columns: half of them from each half of the tile
+    const int cw = wc * (BC / 2 / WC);
+    const auto qrow = [](int f) { return (f / (NC / 2)) * (BC / 2) + f % (NC / 2) * 16; };
+    R lr;
+    Q lq;
+    lr.init(p.r, r0, wr * (BR / WR), lane, wid);
+    lq.init(p.q, c0, cw, lane, wid);
+    constexpr int L = R::NL + Q::NL;
+    const int steps = (int)((p.k + KS - 1) / KS), all = steps * p.parts;
+    // the steps are staged in turn: where the next one starts
+    const uint16_t *rp = lr.base, *qp = lq.base;
+    int at = 0, part = 0;
+    const auto advance = [&]() {
+        rp += lr.step;
+        qp += lq.step;
+        if (++at == steps) {
+            at = 0;
+            rp = lr.base + ++part * p.part;
+            qp = lq.base;
         }
     };
-    stage(rbuf0, qbuf0, 0);
-    for (int s = 0; s < all; s += 2) {
-        step(rbuf0, qbuf0, rbuf1, qbuf1, s);
-        if (s + 1 < all) step(rbuf1, qbuf1, rbuf0, qbuf0, s + 1);
-    }
+    const auto stage = [&](uint8_t *to, int i) {   // load i of the wave
+        const int left = part < p.parts ? (int)min(p.k - (int64_t)at * KS, (int64_t)KS) : 0;
+        if (i < R::NL)
+            lr.load(to, i, wid, rp, left);
+        else
+            lq.load(to + R::BYTES, i - R::NL, wid, qp, left);
+        if (i == L - 1) advance();
+    };
+    struct Fragments {
+        bf16x8 r[CH][NR], q[CH][NC];
+    };
+    const auto read = [&](const uint8_t *from, Fragments &f, int i) {   // fragment i of a step
+        const int c = i / (NR + NC), j = i % (NR + NC);
+        if (j < NC)
+            f.q[c][j] = lq.fragment(from + R::BYTES, qrow(j), c);
+        else
+            f.r[c][j - NC] = lr.fragment(from, 16 * (j - NC), c);
+    };
+
+    f32x4 acc[NC][NR] = {};
+    const auto step = [&](const Fragments &f, Fragments &next, uint8_t *mine, const uint8_t *after) {
+        // the next step's operands have arrived (behind them NB - 2 steps' are
+        // under way), and this step's fragments: every wave's after the barrier
+        __builtin_amdgcn_s_waitcnt(0x0070 | ((NB - 2) * L & 15) | ((NB - 2) * L >> 4) << 14);   // lgkmcnt(0) too
+        barrier_only();
+        constexpr int READS = CH * (NR + NC), GROUPS = CH * NR;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {   // NC matrix instructions, and a share of the rest
+#pragma unroll
+            for (int i = g * L / GROUPS; i < (g + 1) * L / GROUPS; ++i) stage(mine, i);
+#pragma unroll
+            for (int i = g * READS / GROUPS; i < (g + 1) * READS / GROUPS; ++i) read(after, next, i);
+            const int c = g / NR, m = g % NR;
+#pragma unroll
+            for (int n = 0; n < NC; ++n) acc[n][m] = mfma(f.q[c][n], f.r[c][m], acc[n][m]);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int i = 0; i < L; ++i) stage(buf(j), i);
+    wait_loads<(NB - 1) * L>();
+    barrier_only();
+    Fragments f[2];
+#pragma unroll
+    for (int i = 0; i < CH * (NR + NC); ++i) read(buf0, f[0], i);
+    constexpr int TURN = NB % 2 ? 2 * NB : NB;
+    // whole turns: steps past the last one multiply zeros
+    for (int s = 0; s < all; s += TURN)
+#pragma unroll
+        for (int j = 0; j < TURN; ++j) step(f[j % 2], f[(j + 1) % 2], buf(j), buf(j + 1));
     wait_loads<0>();
 
-    const int r16 = lane & 15, quad = lane >> 4;
+    // pairs of groups of columns; the residual's values are all on their way before the first is used
+    const int r16 = lane & 15, quad = lane >> 4, column = cw + Eight::column(quad);
+    constexpr int PAIRS = NC / 2;
+    vec16 residual[PAIRS][NR] = {};
+    const auto row = [&](int m) { return r0 + wr * (BR / WR) + 16 * m + r16; };
+    const auto inside = [&](int f, int m) {
+        return row(m) < p.r.rows && c0 + column + qrow(2 * f) < p.out_ld && (!p.gated || f < PAIRS / 2);
+    };
+    if (p.residual)
 #pragma unroll
-    for (int m = 0; m < NR; ++m) {
-        const int64_t r = r0 + wr * (BR / WR) + 16 * m + r16;
-        if (r >= p.r.rows) continue;
+        for (int f = 0; f < PAIRS; ++f)
 #pragma unroll
-        for (int f = 0; f < NC / 2; ++f) {
-            const int64_t c = c0 + qrow(f) + 4 * quad, c2 = c + BC / 2;
-            if (p.gated) {
-                if (c < p.out_ld) finish4(p, r, c, acc[f][m], acc[f + NC / 2][m]);
-            } else {
-                if (c < p.out_ld) finish4(p, r, c, acc[f][m], f32x4{});
-                if (c2 < p.out_ld) finish4(p, r, c2, acc[f + NC / 2][m], f32x4{});
-            }
+            for (int m = 0; m < NR; ++m)
+                if (inside(f, m)) residual[f][m] = ld16(p.residual + row(m) * p.out_ld + c0 + column + qrow(2 * f));
+#pragma unroll
+    for (int f = 0; f < PAIRS; ++f) {
+        if (p.gated && f >= PAIRS / 2) break;
+#pragma unroll
+        for (int m = 0; m < NR; ++m) {
+            const Eight v(acc[2 * f][m], acc[2 * f + 1][m]);
+            constexpr int HALF = NC / 2;
+            const Eight u(acc[(2 * f + HALF) % NC][m], acc[(2 * f + 1 + HALF) % NC][m]);
+            if (inside(f, m)) finish(p, row(m), c0 + column + qrow(2 * f), v, u, residual[f][m]);
         }
     }
 }
 
-template <bool TR, bool TQ, int BR, int BC, int WR, int WC>
+template <bool TR, bool TQ, int BR, int BC, int WR, int WC, int KS, int NB>
 hipError_t launch_tile(Product p, hipStream_t stream) {
     const int cols = p.gated ? BC / 2 : BC;
     p.rtiles = (int)((p.r.rows + BR - 1) / BR);
     p.ctiles = (int)((p.out_ld + cols - 1) / cols);
-    hipLaunchKernelGGL((ep_linear_tile_kernel<TR, TQ, BR, BC, WR, WC>),
+    hipLaunchKernelGGL((ep_linear_tile_kernel<TR, TQ, BR, BC, WR, WC, KS, NB>),
                        dim3((unsigned)TileOrder::blocks(p.rtiles, p.ctiles)), dim3(64 * WR * WC), 0, stream, p);
     return hipGetLastError();
 }
 
 template <bool TR, bool TQ>
 hipError_t launch_product(const Product &p, hipStream_t stream) {
-    return launch_tile<TR, TQ, 64, 64, 2, 2>(p, stream);
+    const int64_t cols = p.gated ? 2 * p.out_ld : p.out_ld;
+    const auto tiles = [&](int BR, int BC) { return ((p.r.rows + BR - 1) / BR) * ((cols + BC - 1) / BC); };
+    if (tiles(256, 256) >= 160) return launch_tile<TR, TQ, 256, 256, 2, 4, 32, 4>(p, stream);
+    if (tiles(128, 128) >= 160) return launch_tile<TR, TQ, 128, 128, 2, 2, 32, 4>(p, stream);
+    return launch_tile<TR, TQ, 64, 64, 4, 1, 64, 4>(p, stream);
+}
+
+// ---------------------------------------------------------------- few rows
+
+// One block: 16 G weight rows (gated: 8 G of each half) by up to 16 MT rows of
+// x, NW waves with a part of K each; the weights' bytes are the time.
+template <bool GATED, int G, int MT, int NW, int NB>
+__global__ __launch_bounds__(64 * NW) void ep_linear_stream_kernel(Product p, int ctiles) {
+    typedef Step<false, G> S;
+    constexpr int KE = S::KE, C = S::CHUNKS;
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[NW * G * 2048];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[NW * G * 2048];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[NB > 2 ? NW * G * 2048 : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t buf3[NB > 3 ? NW * G * 2048 : 16];
+    static_assert(NB == 2 || NB == 4, "as many buffers");
+    const auto buf = [&](int j) {
+        return j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : (j % NB == 2 ? buf2 : buf3));
+    };
+    const int c0 = (int)(blockIdx.x % ctiles) * (GATED ? 8 * G : 16 * G);
+    const int64_t r0 = (int64_t)(blockIdx.x / ctiles) * 16 * MT;
+    const int rows = (int)min(p.r.rows - r0, (int64_t)16 * MT);
+    const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int r16 = lane & 15, quad = lane >> 4;
+    const uint32_t kbytes = (uint32_t)p.k * 2;
+    const int KU = ((int)p.k + KE - 1) / KE;
+    const int first = KU * wid / NW, n = KU * (wid + 1) / NW - first;
+
+    // gated: the first half of the LDS rows is the gate's, the second its factor's
+    const uint16_t *w0 = p.q.p + (int64_t)c0 * p.q.ld, *w1 = GATED ? w0 + p.q.split * p.q.ld : w0;
+    const rsrc_t b0 = buffer(w0), b1 = buffer(w1);
+    const int last = (int)p.out_ld - 1 - c0;
+    uint32_t woff[2 * G];
+    const int srow = lane >> 3;
+    const uint32_t piece = (uint32_t)(((lane & 7) ^ srow) << 4);
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) woff[i] = (uint32_t)min(srow + 8 * (GATED ? i % G : i), last) * kbytes + piece;
+    const auto stage = [&](uint8_t *to, int i) {
+        const uint32_t k = (uint32_t)(first + i) * 128, past = i < n && k + piece < kbytes ? 0u : kPast;
+#pragma unroll
+        for (int j = 0; j < 2 * G; ++j)
+            load_to_lds(GATED && j >= G ? b1 : b0, to + wid * (G * 2048) + j * 1024, woff[j] | past, i < n ? k : 0u);
+    };
+    const rsrc_t xb = buffer(p.r.p + r0 * p.r.ld);
+    uint32_t xoff[MT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xoff[m] = 16 * m + r16 < rows ? (uint32_t)(16 * m + r16) * kbytes : kPast;
+    struct Values {
+        vec16 v[MT][C];
+    };
+    const auto load_x = [&](int i, Values &to) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const uint32_t at = (uint32_t)(first + i) * 128 + S::at(c, quad);
+                to.v[m][c] = load_16(xb, i < n && at < kbytes ? xoff[m] + at : kPast, 0);
+            }
+    };
+    f32x4 acc[G][MT] = {};
+    const uint32_t plo = (uint32_t)(r16 * 128 + ((quad ^ (r16 & 7)) << 4));
+    const auto step = [&](uint8_t *b, const Values &x, Values &next, int i) {
+        wait_step<NB, MT * C, 2 * G>(i);
+        const S a(b + wid * (G * 2048), plo);
+        __builtin_amdgcn_sched_barrier(0);
+        load_x(i + 1, next);
+        __builtin_amdgcn_sched_barrier(0);
+        stage(b, i + NB);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                    acc[g][m] = mfma(a.a[g][c], __builtin_bit_cast(bf16x8, x.v[m][c]), acc[g][m]);
+    };
+    Values v[2];
+    stage(buf0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_x(0, v[0]);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 1; j < NB; ++j) stage(buf(j), j);
+    for (int i = 0; i < n; i += NB) {
+#pragma unroll
+        for (int j = 0; j < NB; ++j)
+            if (j == 0 || i + j < n) step(buf(j), v[j % 2], v[(j + 1) % 2], i + j);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);
+
+    // the parts of K are added in their order: a tile of rows by one wave each
+    __syncthreads();
+    static_assert(MT <= 2 * NB && MT <= NW, "they fit, and a wave for each");
+    const auto part = [&](int m) { return reinterpret_cast<f32x4 *>(buf(m / 2)) + m % 2 * (NW * G * kWave) + lane; };
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int g = 0; g < G; ++g) part(m)[(wid * G + g) * kWave] = acc[g][m];
+    __syncthreads();
+    if (wid >= MT) return;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        if (m != wid) continue;
+        f32x4 sum[G] = {};
+#pragma unroll
+        for (int q = 0; q < NW; ++q)
+#pragma unroll
+            for (int g = 0; g < G; ++g) sum[g] += part(m)[(q * G + g) * kWave];
+        const int r = 16 * m + r16;
+        vec16 residual = {};
+        if constexpr (GATED || G == 1) {
+            // the lane's 4 columns and its neighbour's 4 (a quad on)
+            const f32x4 &u = sum[G - 1];
+            const Eight v(sum[0], sum[0]);
+            Eight w(u, u);
+            // one group of weight rows: gate in quads 0 and 1, factors in quads 2 and 3
+            if constexpr (GATED && G == 1)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w.v[i] = __shfl_xor(v.v[i], 32);
+            const int c = c0 + 8 * (quad >> 1);
+            if (r < rows && quad % 2 == 0 && (!GATED || G > 1 || quad == 0) && c < p.out_ld) {
+                if (p.residual) residual = ld16(p.residual + (r0 + r) * p.out_ld + c);
+                finish(p, r0 + r, c, v, w, residual);
+            }
+        } else {
+            const int c = c0 + Eight::column(quad);
+            const Eight v(sum[0], sum[G - 1]);
+            if (r < rows && c < p.out_ld) {
+                if (p.residual) residual = ld16(p.residual + (r0 + r) * p.out_ld + c);
+                finish(p, r0 + r, c, v, v, residual);
+            }
+        }
+    }
+}
+
+template <bool GATED, int G, int MT, int NW, int NB>
+hipError_t launch_stream(const Product &p, hipStream_t stream) {
+    const int wide = GATED ? 8 * G : 16 * G, ctiles = (int)((p.out_ld + wide - 1) / wide);
+    const int64_t blocks = ctiles * ((p.r.rows + 16 * MT - 1) / (16 * MT));
+    hipLaunchKernelGGL((ep_linear_stream_kernel<GATED, G, MT, NW, NB>), dim3((unsigned)blocks), dim3(64 * NW), 0, stream,
+                       p, ctiles);
+    return hipGetLastError();
+}
+
+template <bool GATED, int MT>
+hipError_t launch_stream(const Product &p, hipStream_t stream) {
+    if ((GATED ? 2 : 1) * p.out_ld >= 32 * 256) return launch_stream<GATED, 2, MT, 8, 2>(p, stream);
+    return launch_stream<GATED, 1, MT, 16, 4>(p, stream);
 }
 
 // ---------------------------------------------------------------- the gradient over z
 
-// dz from dy and z in bf16 (in one part, or in two: the rounded value and its
-// rounded rest) and the sums of its columns over runs of kDzRows rows, for the
-// bias.  A wave's lanes take 8 columns each, its 4 waves rows in turn.
+// dz from dy and z in bf16 (in one part, or in three: the rounded value, its
+// rounded rest and the rest of that, together the binary32 value) and the sums of
+// its columns over runs of kDzRows rows, for the bias.  A wave's lanes take 8
+// columns each, its 4 waves rows in turn, 4 at a time so that their loads are
+// under way together.
 constexpr int kDzThreads = 256;
 template <typename Dy>
 __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s, const Dy *__restrict__ dy,
                                                                   const uint16_t *__restrict__ z,
                                                                   uint16_t *__restrict__ dz, int parts,
                                                                   float *__restrict__ sums) {
-    constexpr int W = kDzThreads / kWave;
+    constexpr int W = kDzThreads / kWave, D = sizeof(Dy) / 2, AT_ONCE = 4;
+    static_assert(kDzRows % (W * AT_ONCE) == 0, "whole turns");
     __shared__ float part[W][2][8][kWave];
     const int lane = threadIdx.x & (kWave - 1), wid = threadIdx.x / kWave;
     const int cols = (s.N + 511) / 512, ct = blockIdx.x % cols;
     const int64_t run = blockIdx.x / cols;
     const int c = (ct * kWave + lane) * 8, wide = s.wide();
     const int64_t plane = s.M * wide;
+    const bool kept = s.act != kActNone || s.gated;
     float sum[2][8] = {};
     const auto unpack = [](vec16 v, float (&f)[8]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(v[i]), f[2 * i + 1] = bf16_hi(v[i]);
     };
-    const auto store = [&](int64_t at, const float (&f)[8]) {
-        vec16 hi, lo;
+    const auto store = [&](int64_t at, float (&f)[8]) {
+        for (int n = 0; n < parts; ++n) {
+            vec16 out;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t h[2], l[2];
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h[2];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float v = f[2 * i + j];
-                h[j] = f32_to_bf16(v);
-                // of two parts the first stays finite where the value is
-                if (parts > 1 && (h[j] & 0x7FFF) == 0x7F80 && v - v == 0.0f) h[j] = f2u(v) >> 16;
-                const float rest = v - u2f(h[j] << 16);
-                l[j] = (h[j] & 0x7F80) == 0x7F80 ? 0u : f32_to_bf16(rest);
+                for (int j = 0; j < 2; ++j) {
+                    float &v = f[2 * i + j];
+                    h[j] = f32_to_bf16(v);
+                    // of several parts the first stays finite where the value is
+                    if (parts > 1 && (h[j] & 0x7FFF) == 0x7F80 && v - v == 0.0f) h[j] = f2u(v) >> 16;
+                    v = (h[j] & 0x7F80) == 0x7F80 ? 0.0f : v - u2f(h[j] << 16);
+                }
+                out[i] = h[0] | h[1] << 16;
             }
-            hi[i] = h[0] | h[1] << 16;
-            lo[i] = l[0] | l[1] << 16;
+            st16(dz + n * plane + at, out);
         }
-        st16(dz + at, hi);
-        if (parts > 1) st16(dz + plane + at, lo);
     };
-    if (c < s.N)
-        for (int i = wid; i < kDzRows; i += W) {
-            const int64_t r = run * kDzRows + i;
-            if (r >= s.M) break;
-            float g[8], a[8], b[8] = {};
-            if constexpr (sizeof(Dy) == 4) {
-                const f32x4 lo = *reinterpret_cast<const f32x4 *>(dy + r * s.N + c),
-                            hi = *reinterpret_cast<const f32x4 *>(dy + r * s.N + c + 4);
+    for (int i0 = 0; i0 < kDzRows; i0 += W * AT_ONCE) {
+        vec16 gv[AT_ONCE][D] = {}, zv[AT_ONCE] = {}, uv[AT_ONCE] = {};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) g[j] = lo[j], g[4 + j] = hi[j];
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int64_t r = run * kDzRows + i0 + i * W + wid;
+            if (r >= s.M || c >= s.N) continue;
+#pragma unroll
+            for (int j = 0; j < D; ++j) gv[i][j] = ld16(dy + r * s.N + c + 8 / D * j);
+            if (kept) zv[i] = ld16(z + r * wide + c);
+            if (s.gated) uv[i] = ld16(z + r * wide + s.N + c);
+        }
+#pragma unroll
+        for (int i = 0; i < AT_ONCE; ++i) {
+            const int64_t r = run * kDzRows + i0 + i * W + wid;
+            if (r >= s.M || c >= s.N) continue;
+            float g[8], a[8], b[8] = {}, v[8], u[8];
+            if constexpr (D == 2) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) g[j] = u2f(gv[i][j / 4][j % 4]);
             } else {
-                unpack(ld16(dy + r * s.N + c), g);
+                unpack(gv[i][0], g);
             }
-            if (s.act != kActNone || s.gated) {
-                float v[8], u[8];
-                unpack(ld16(z + r * wide + c), v);
-                if (s.gated) unpack(ld16(z + r * wide + s.N + c), u);
-                with_activation(s.act, [&](auto act) {
+            unpack(zv[i], v);
+            unpack(uv[i], u);
+            with_activation(s.act, [&](auto act) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float f, d;
-                        derive<decltype(act)::value>(v[j], &f, &d);
-                        a[j] = s.gated ? g[j] * u[j] * d : g[j] * d;
-                        b[j] = g[j] * f;
-                    }
-                });
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) a[j] = g[j];
-            }
-            if (parts > 0) {
-                store(r * wide + c, a);
-                if (s.gated) store(r * wide + s.N + c, b);
-            }
+                for (int j = 0; j < 8; ++j) {
+                    float f, d;
+                    derive<decltype(act)::value>(v[j], &f, &d);
+                    a[j] = s.gated ? g[j] * u[j] * d : g[j] * d;
+                    if (s.gated) b[j] = g[j] * f;
+                }
+            });
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[0][j] += a[j], sum[1][j] += b[j];
+            store(r * wide + c, a);
+            if (s.gated) store(r * wide + s.N + c, b);
         }
+    }
     if (!sums) return;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -410,13 +655,21 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
     }
 }
 
-// The runs' sums, added in order; with none, 0.
+// The runs' sums: 16 threads to a column, each with a 16th of the runs, added in
+// order; with no runs, 0.
 __global__ __launch_bounds__(256) void ep_linear_bias_kernel(const float *__restrict__ sums, int64_t runs, int wide,
                                                              float *__restrict__ out) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= wide) return;
+    __shared__ float part[16][16];
+    const int lane = threadIdx.x % 16, group = threadIdx.x / 16, c = blockIdx.x * 16 + lane;
     float v = 0.0f;
-    for (int64_t i = 0; i < runs; ++i) v += sums[i * wide + c];
+    if (c < wide)
+        for (int64_t i = runs * group / 16; i < runs * (group + 1) / 16; ++i) v += sums[i * wide + c];
+    part[group][lane] = v;
+    __syncthreads();
+    if (group > 0 || c >= wide) return;
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v += part[i][lane];
     out[c] = v;
 }
 
@@ -443,6 +696,9 @@ hipError_t launch_linear(const LinearShape &s, const uint16_t *x, const uint16_t
     p.act = s.act;
     p.gated = s.gated;
     p.linear = true;
+    if (s.M <= 16) return s.gated ? launch_stream<true, 1>(p, stream) : launch_stream<false, 1>(p, stream);
+    if (s.M <= 32) return s.gated ? launch_stream<true, 2>(p, stream) : launch_stream<false, 2>(p, stream);
+    if (s.M <= 64) return s.gated ? launch_stream<true, 4>(p, stream) : launch_stream<false, 4>(p, stream);
     return launch_product<false, false>(p, stream);
 }
 
@@ -457,12 +713,12 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
                                static_cast<vec16 *>(grad_w), n);
         }
         if (grad_bias)
-            hipLaunchKernelGGL(ep_linear_bias_kernel, dim3((unsigned)((wide + 255) / 256)), dim3(256), 0, stream,
+            hipLaunchKernelGGL(ep_linear_bias_kernel, dim3((unsigned)((wide + 15) / 16)), dim3(256), 0, stream,
                                nullptr, 0, wide, grad_bias);
-        return hipGetLastError();
+        return grad_w || grad_bias ? hipGetLastError() : hipSuccess;
     }
-    // two parts only for the product that takes them
-    const int parts = s.plain() ? 0 : (s.w32 && grad_w ? 2 : 1);
+    // three parts only for the product that takes them
+    const int parts = s.plain() ? 0 : (s.w32 && grad_w ? 3 : 1);
     uint16_t *dz = reinterpret_cast<uint16_t *>(ws);
     float *sums = reinterpret_cast<float *>(ws + linear_sums_offset(s));
     const int64_t runs = (s.M + kDzRows - 1) / kDzRows;
@@ -476,9 +732,9 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
                                static_cast<const uint16_t *>(dy), z, dz, parts, grad_bias ? sums : nullptr);
     }
     if (grad_bias)
-        hipLaunchKernelGGL(ep_linear_bias_kernel, dim3((unsigned)((wide + 255) / 256)), dim3(256), 0, stream, sums,
+        hipLaunchKernelGGL(ep_linear_bias_kernel, dim3((unsigned)((wide + 15) / 16)), dim3(256), 0, stream, sums,
                            runs, wide, grad_bias);
-    hipError_t e = hipGetLastError();
+    hipError_t e = grad_x || grad_w || grad_bias ? hipGetLastError() : hipSuccess;
     if (e != hipSuccess) return e;
     const uint16_t *d = parts > 0 ? dz : static_cast<const uint16_t *>(dy);
     if (grad_x) {
@@ -497,7 +753,7 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
         p.r = {d, wide, wide, 0};
         p.q = {x, s.K, s.K, 0};
         p.k = s.M;
-        p.parts = parts > 1 ? 2 : 1;
+        p.parts = parts > 1 ? parts : 1;
         p.part = s.M * wide;
         p.out_ld = s.K;
         p.out = grad_w;

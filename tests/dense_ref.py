@@ -102,8 +102,8 @@ def slope_error(z, act):
 
 
 def linear_backward(dy, x, w, z, act, gated, parts):
-    """(grad_x, its error), (grad_w, ...), (grad_bias, ...); parts: how grad_w takes dz (0: as it is, 1: bf16, 2: two
-    bf16 parts; grad_x takes the first)."""
+    """(grad_x, its error), (grad_w, ...), (grad_bias, ...); parts: how grad_w takes dz (0: as it is, 1: bf16, 3: three
+    bf16 parts, exactly; grad_x takes the first)."""
     dy, x, w = dy.double(), x.double(), w.double()
     if gated:
         n = dy.shape[1]
@@ -120,14 +120,14 @@ def linear_backward(dy, x, w, z, act, gated, parts):
         dz, e = dy, torch.zeros_like(dy)
     tiny = 2.0 ** -134
     ex = e + (0 if parts == 0 else BF16_HALF * (dz.abs() + e) + tiny)
-    ew = e + (0, BF16_HALF, 2.0 ** -16)[parts] * (dz.abs() + e) + (tiny if parts else 0)
+    ew = e + (BF16_HALF if parts == 1 else 0) * (dz.abs() + e) + (tiny if parts else 0)
     gx, gw = dz @ w, dz.T @ x
     mx, mw = (dz.abs() + ex) @ w.abs(), (dz.abs() + ew).T @ x.abs()
     ex = ex @ w.abs() + sum_error(mx, w.shape[0])
     ew = ew.T @ x.abs() + sum_error(mw, max(parts, 1) * x.shape[0])
     gb, mb = dz.sum(0), dz.abs().sum(0)
-    # runs of 64 rows, 16 of a wave's and 4 waves', then the runs in turn
-    eb = e.sum(0) + STEP * (16 + 4 + len(dz) / 64 + 1) * (mb + e.sum(0))
+    # runs of 32 rows, 8 of a wave's and 4 waves', then 16 parts of the runs
+    eb = e.sum(0) + STEP * (8 + 4 + len(dz) / 512 + 1 + 16) * (mb + e.sum(0))
     return (gx, ex), (gw, ew), (gb, eb)
 
 

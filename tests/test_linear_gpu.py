@@ -67,7 +67,7 @@ def test_backward(ep, M, K, N, act, gated, f32, w32):
     kw = dict(activation=act, gated=gated, grad_w_dtype=F32 if w32 else BF)
     gx, gw, gb = ep.linear_backward(*c.values(), bias=True, **kw)
     plain = act is None and not gated and not f32
-    (wx, ex), (ww, ew), (wb, eb) = ref.linear_backward(dy, d["x"], d["w"], z, act, gated, 0 if plain else 1 + w32)
+    (wx, ex), (ww, ew), (wb, eb) = ref.linear_backward(dy, d["x"], d["w"], z, act, gated, 0 if plain else (3 if w32 else 1))
     ref.check(gx.cpu(), wx, ex, ref.BF16_HALF)
     ref.check(gw.cpu(), ww, ew, ref.F32_HALF if w32 else ref.BF16_HALF)
     ref.check(gb.cpu(), wb, eb, ref.F32_HALF)
@@ -195,3 +195,25 @@ def test_refusals(ep):
         ep.linear_backward(torch.zeros(8, 16, device="cuda").to(BF), x, w, activation="silu")
     with pytest.raises(RuntimeError, match="workspace"):
         ep.linear_backward(torch.zeros(8, 16, device="cuda"), x, w, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("M,K,N,act,gated", [(4100, 200, 2600, "silu", True), (5000, 96, 2056, "gelu", False),
+                                             (1600, 1608, 1800, None, False), (2050, 520, 1040, "silu", True),
+                                             (700, 4104, 5000, "relu", False)], ids=str)
+def test_large_tiles(ep, M, K, N, act, gated):
+    """Enough rows and columns for the wider tiles of each product, with ragged ends."""
+    d = _draw(M, K, N, gated, True, not gated, seed=4)
+    c = _cuda(d)
+    y, z = ep.linear(*c.values(), activation=act, gated=gated, save=True)
+    wy, ey, wz, ez = ref.linear(*c.values(), act, gated)
+    ref.check(z, wz, ez, ref.BF16_HALF)
+    ref.check(y, wy, ey, ref.BF16_HALF)
+    for f32, w32 in ((False, False), (True, True)):
+        dy = torch.randn(M, N, device="cuda").to(F32 if f32 else BF)
+        zz = z if act is not None or gated else None
+        got = ep.linear_backward(dy, c["x"], c["w"], zz, activation=act, gated=gated, bias=True,
+                                 grad_w_dtype=F32 if w32 else BF)
+        plain = zz is None and not f32
+        want = ref.linear_backward(dy, c["x"], c["w"], zz, act, gated, 0 if plain else (3 if w32 else 1))
+        for g, (v, e), half in zip(got, want, (ref.BF16_HALF, ref.F32_HALF if w32 else ref.BF16_HALF, ref.F32_HALF)):
+            ref.check(g, v, e, half)
