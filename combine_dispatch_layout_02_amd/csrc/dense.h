@@ -29,10 +29,26 @@ struct FewSegment {
 };
 static_assert(sizeof(FewSegment) == 64, "one line");
 
-// Workspace: the number of segments, the segments, h as two bf16 parts [T k][2][I].
-constexpr size_t kFewHead = 256;
+// The second kernel's blocks have 32 columns of y.  Where those are fewer than
+// the chip's CUs, each has several blocks with a part of the segments, and the
+// last of them adds up the parts.
+constexpr int kFewColumns = 32, kFewJoins = 128;
+inline int few_columns(const FewShape &s) { return (s.H + kFewColumns - 1) / kFewColumns; }
+inline int few_parts(const FewShape &s) {
+    const int cols = few_columns(s), most = s.T * s.k;   // as many as there can be segments
+    const int parts = cols <= kFewJoins ? (256 / cols < 16 ? 256 / cols : 16) : 1;
+    return parts < most ? parts : most;
+}
+
+// Workspace: the number of segments, the counts of blocks that are done, the
+// segments, h as two bf16 parts [T k][2][I], the parts of y [parts][T][H].
+constexpr size_t kFewHead = 256 + kFewJoins * 4;
 inline size_t few_h_offset(const FewShape &s) { return kFewHead + (size_t)s.T * s.k * sizeof(FewSegment); }
-inline size_t few_workspace(const FewShape &s) { return few_h_offset(s) + (size_t)s.T * s.k * s.I * 4; }
+inline size_t few_partial_offset(const FewShape &s) { return few_h_offset(s) + (size_t)s.T * s.k * s.I * 4; }
+inline size_t few_workspace(const FewShape &s) {
+    const int parts = s.T > 0 ? few_parts(s) : 1;
+    return few_partial_offset(s) + (parts > 1 ? (size_t)parts * s.T * s.H * 4 : 0);
+}
 
 hipError_t launch_few(const FewShape &s, const uint16_t *x, const int64_t *idx, const float *w, const void *up,
                       const float *ups, const void *down, const float *downs, const uint16_t *residual, uint16_t *y,

@@ -26,7 +26,8 @@ namespace {
 // ---------------------------------------------------------------- the segments
 
 // Which expert has which rows, for the second kernel: one block, experts
-// ascending, each one's tokens ascending, 16 a segment.
+// ascending, each one's tokens ascending, 16 a segment.  It also clears that
+// kernel's counts of blocks that are done.
 constexpr int kPlanThreads = 256;
 struct Plan {
     uint32_t used[128];              // a bit for every expert
@@ -35,9 +36,11 @@ struct Plan {
     uint16_t first[kFewTokens * 32]; // segments, then the first of each
     int total;
 };
-__device__ void make_plan(Plan &p, const FewShape &s, const int64_t *idx, int32_t *count, FewSegment *seg) {
+__device__ void make_plan(Plan &p, const FewShape &s, const int64_t *idx, int32_t *count, FewSegment *seg,
+                          int32_t *arrived) {
     const int tid = threadIdx.x, lane = tid & (kWave - 1), wid = tid / kWave, pairs = s.T * s.k;
     if (tid < 128) p.used[tid] = 0;
+    if (tid < kFewJoins) arrived[tid] = 0;
     __syncthreads();
     for (int i = tid; i < pairs; i += kPlanThreads) {
         const int64_t e = idx[i];
@@ -106,32 +109,31 @@ __device__ void make_plan(Plan &p, const FewShape &s, const int64_t *idx, int32_
 
 // ---------------------------------------------------------------- gate and up
 
-// One block: 16 columns of h (16 gate and the same 16 up rows of the weights)
-// for up to 16 MT tokens of one expert; NW waves, each with a part of K.  The
+// One block: 16 GU columns of h (those gate and up rows of the weights) for up
+// to 16 MT tokens of one expert; NW waves, each with a part of K.  The
 // grid has a block column for every pair (t, j); the block whose pair is the
 // first of its expert's (or of the next 16 MT tokens of it) does the work.
-template <bool F8, int MT, int NW, int NB>
+template <bool F8, int GU, int MT, int NW, int NB>
 __global__ __launch_bounds__(64 * NW) void ep_few_up_kernel(
     FewShape s, const uint16_t *__restrict__ x, const int64_t *__restrict__ idx, const float *__restrict__ w,
-    const uint8_t *__restrict__ up, const float *__restrict__ ups, int32_t *count, FewSegment *seg,
+    const uint8_t *__restrict__ up, const float *__restrict__ ups, int32_t *count, FewSegment *seg, int32_t *arrived,
     uint16_t *__restrict__ h, int cols) {
-    typedef Step<F8, 2> S;
-    constexpr int KE = S::KE, C = S::CHUNKS;
-    __shared__ __attribute__((aligned(16))) uint8_t buf0[NW * 4096];
-    __shared__ __attribute__((aligned(16))) uint8_t buf1[NW * 4096];
-    __shared__ __attribute__((aligned(16))) uint8_t buf2[NB > 2 ? NW * 4096 : 16];
-    static_assert(NB == 2 || NB == 3, "as many buffers");
-    const auto buf = [&](int j) { return j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : buf2); };
+    typedef Step<F8, 2 * GU> S;
+    constexpr int KE = S::KE, C = S::CHUNKS, BYTES = GU * 4096;   // of a wave's step
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[NW * BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[NW * BYTES];
+    static_assert(NB == 2, "as many buffers");
+    const auto buf = [&](int j) { return j % NB == 0 ? buf0 : buf1; };
     __shared__ int32_t rows_pair[16 * MT];
     __shared__ float rows_w[16 * MT];
     static_assert(sizeof(Plan) <= sizeof(buf0), "the plan uses the buffer");
     static_assert(64 * NW == kPlanThreads, "the plan's block");
 
     if (blockIdx.x == 0) {
-        make_plan(*reinterpret_cast<Plan *>(buf0), s, idx, count, seg);
+        make_plan(*reinterpret_cast<Plan *>(buf0), s, idx, count, seg, arrived);
         return;
     }
-    const int p = (blockIdx.x - 1) / cols, n0 = (int)((blockIdx.x - 1) % cols) * 16;
+    const int p = (blockIdx.x - 1) / cols, n0 = (int)((blockIdx.x - 1) % cols) * 16 * GU;
     const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int r16 = lane & 15, quad = lane >> 4;
 
@@ -167,14 +169,14 @@ __global__ __launch_bounds__(64 * NW) void ep_few_up_kernel(
     const uint8_t *we = up + (size_t)e * 2 * s.I * kbytes;
     const int last = s.I - 1 - n0;   // columns past the end repeat the last one
     const rsrc_t gb = buffer(we + (size_t)n0 * kbytes), ub = buffer(we + ((size_t)s.I + n0) * kbytes);
-    Stage<2> st;
+    Stage<2 * GU> st;
     const int srow = lane >> 3;
     st.piece = (uint32_t)(((lane & 7) ^ srow) << 4);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) st.off[i] = (uint32_t)min(srow + 8 * (i & 1), last) * kbytes;
+    for (int i = 0; i < 4 * GU; ++i) st.off[i] = (uint32_t)min(srow + 8 * (i % (2 * GU)), last) * kbytes;
     const auto stage = [&](uint8_t *buf, int i) {
         const uint32_t k = i < n ? (uint32_t)(first + i) * 128 : 0u;
-        st.go(gb, ub, buf + wid * 4096, k, i < n ? kbytes : 0u);
+        st.go(gb, ub, buf + wid * BYTES, k, i < n ? kbytes : 0u);
     };
     // the tokens' rows, straight into the operands' layout
     const rsrc_t xb = buffer(x, (int64_t)s.T * s.H * 2);
@@ -184,7 +186,6 @@ __global__ __launch_bounds__(64 * NW) void ep_few_up_kernel(
         xoff[m] = 16 * m + r16 < rows ? (uint32_t)(rows_pair[16 * m + r16] / s.k) * (uint32_t)s.H * 2 : kPast;
     struct Values {
         vec16 v[MT][C];
-        float scale[2];
     };
     const auto load_x = [&](int i, Values &to) {
         const uint32_t k = (uint32_t)(first + i) * (KE * 2);
@@ -199,74 +200,82 @@ __global__ __launch_bounds__(64 * NW) void ep_few_up_kernel(
     const int KB = s.H / 128;   // scales of a row of blocks
     const rsrc_t sb = buffer(F8 ? ups + (size_t)e * (2 * s.I / 128) * KB : nullptr, F8 ? (int64_t)(2 * s.I / 128) * KB * 4 : 0);
     const uint32_t soff[2] = {(uint32_t)(n0 / 128) * KB * 4, (uint32_t)((s.I + n0) / 128) * KB * 4};
-    const auto scales = [&](int i, Values &to) {
+    // of 4 steps at a time; the columns of a block lie in one of the scales' blocks
+    f32x4 sc[2] = {}, nsc[2] = {};
+    const auto scales = [&](int i) {
         if constexpr (F8)
 #pragma unroll
-            for (int g = 0; g < 2; ++g) to.scale[g] = load_f32(sb, soff[g], (uint32_t)min(first + i, KB - 1) * 4);
+            for (int g = 0; g < 2; ++g) nsc[g] = load_4f32(sb, soff[g] + (uint32_t)(first + i) * 4, 0);
     };
 
-    f32x4 acc[2][MT] = {};
+    f32x4 acc[2 * GU][MT] = {};
     const uint32_t plo = (uint32_t)(r16 * 128 + ((quad ^ (r16 & 7)) << 4));
-    const auto step = [&](uint8_t *buf, const Values &x, Values &next, int i) {
-        wait_step<NB, MT * C + (F8 ? 2 : 0), 4>(i);
-        const uint8_t *p = buf + wid * 4096;
-        const S a(p, plo);   // the operands are in registers: their place takes the step NB on
+    const auto step = [&](uint8_t *buf, const Values &x, Values &next, int i, int j) {
+        wait_step<NB, MT * C, 4 * GU>(i);
+        const S a(buf + wid * BYTES, plo);   // the operands are in registers: their place takes the step NB on
         __builtin_amdgcn_sched_barrier(0);
         load_x(i + 1, next);
-        scales(i + 1, next);
+        if (j == 0) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g) sc[g] = nsc[g];
+            scales(i + 4);
+        }
         __builtin_amdgcn_sched_barrier(0);
         stage(buf, i + NB);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
             if (m > 0 && rows <= 16 * m) break;   // the same for the whole block
-            f32x4 d[2] = {F8 ? f32x4{} : acc[0][m], F8 ? f32x4{} : acc[1][m]};
+            f32x4 d[2 * GU];
+#pragma unroll
+            for (int g = 0; g < 2 * GU; ++g) d[g] = F8 ? f32x4{} : acc[g][m];
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 const bf16x8 b = __builtin_bit_cast(bf16x8, x.v[m][c]);
-                d[0] = mfma(a.a[0][c], b, d[0]);
-                d[1] = mfma(a.a[1][c], b, d[1]);
+#pragma unroll
+                for (int g = 0; g < 2 * GU; ++g) d[g] = mfma(a.a[g][c], b, d[g]);
             }
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+            for (int g = 0; g < 2 * GU; ++g)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    acc[g][m][q] = F8 ? __builtin_fmaf(d[g][q], x.scale[g], acc[g][m][q]) : d[g][q];
+                    acc[g][m][q] = F8 ? __builtin_fmaf(d[g][q], sc[g / GU][j], acc[g][m][q]) : d[g][q];
         }
     };
     Values v[2];
+    scales(0);
     stage(buf0, 0);
     __builtin_amdgcn_sched_barrier(0);
     load_x(0, v[0]);
-    scales(0, v[0]);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int j = 1; j < NB; ++j) stage(buf(j), j);
-    constexpr int TURN = NB % 2 ? 2 * NB : NB;
-    for (int i = 0; i < n; i += TURN) {
+    for (int i = 0; i < n; i += 4) {
 #pragma unroll
-        for (int j = 0; j < TURN; ++j)
-            if (j == 0 || i + j < n) step(buf(j), v[j % 2], v[(j + 1) % 2], i + j);
+        for (int j = 0; j < 4; ++j)
+            if (j == 0 || i + j < n) step(buf(j), v[j % 2], v[(j + 1) % 2], i + j, j);
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);
 
     // the parts of K are added in their order
     __syncthreads();
-    static_assert((NW - 1) * 2 * MT * 1024 <= NW * 4096, "they fit");
+    static_assert(MT <= 2, "they fit");
+    constexpr int N = 2 * GU * MT;
     f32x4 *part = reinterpret_cast<f32x4 *>(buf0);
     if (wid > 0)
 #pragma unroll
-        for (int m = 0; m < 2 * MT; ++m) part[((wid - 1) * 2 * MT + m) * kWave + lane] = acc[m & 1][m >> 1];
+        for (int i = 0; i < N; ++i) part[((wid - 1) * N + i) * kWave + lane] = acc[i / MT][i % MT];
     __syncthreads();
     if (wid > 0) return;
 #pragma unroll
     for (int q = 0; q < NW - 1; ++q)
 #pragma unroll
-        for (int m = 0; m < 2 * MT; ++m) acc[m & 1][m >> 1] += part[(q * 2 * MT + m) * kWave + lane];
+        for (int i = 0; i < N; ++i) acc[i / MT][i % MT] += part[(q * N + i) * kWave + lane];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
-        const f32x4 v = gates(acc[0][m], acc[1][m]);
-        const int r = 16 * m + r16, col = n0 + 4 * quad;
+    for (int f = 0; f < GU * MT; ++f) {
+        const int g = f / MT, m = f % MT;
+        const f32x4 v = gates(acc[g][m], acc[GU + g][m]);
+        const int r = 16 * m + r16, col = n0 + 16 * g + 4 * quad;
         if (r >= rows || col >= s.I) continue;   // I % 8 == 0: all 4 in or all out
         // h leaves as two bf16 parts, its upper 16 bits and the rounded rest:
         // 2^-17 of it is lost, at 4 bytes a value that the caches hold
@@ -297,7 +306,8 @@ template <bool F8, int RT, int TT, int G, int NW, int NB>
 __global__ __launch_bounds__(64 * NW) void ep_few_down_kernel(
     FewShape s, const int32_t *__restrict__ count, const FewSegment *__restrict__ seg,
     const uint16_t *__restrict__ h, const uint8_t *__restrict__ down, const float *__restrict__ downs,
-    const uint16_t *residual, uint16_t *y) {
+    const uint16_t *residual, uint16_t *y, int cols, int parts, float *__restrict__ partial,
+    int32_t *__restrict__ arrived) {
     typedef Step<F8, G> S;
     constexpr int KE = S::KE, C = S::CHUNKS;
     __shared__ __attribute__((aligned(16))) uint8_t buf0[NW * G * 2048];
@@ -309,13 +319,15 @@ __global__ __launch_bounds__(64 * NW) void ep_few_down_kernel(
         return j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : (j % NB == 2 ? buf2 : buf3));
     };
 
-    const int n0 = blockIdx.x * 16 * G;
+    const int ct = blockIdx.x % cols, bp = blockIdx.x / cols, n0 = ct * 16 * G;
+    __shared__ int last_block;
     const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int r16 = lane & 15, quad = lane >> 4, c8 = r16 & 7, part = r16 >> 3;
+    const int r16 = lane & 15, quad = lane >> 4, c8 = r16 & 7, half = r16 >> 3;
     const uint32_t kbytes = (uint32_t)s.I * (F8 ? 1 : 2);
     const int KU = (s.I + KE - 1) / KE;
     const int total = *count * KU;
-    const int lo = (int)((int64_t)total * wid / NW), hi = (int)((int64_t)total * (wid + 1) / NW);
+    const int at = bp * NW + wid, of = parts * NW;
+    const int lo = (int)((int64_t)total * at / of), hi = (int)((int64_t)total * (at + 1) / of);
 
     Stage<G> st;
     const int srow = lane >> 3, last = s.H - 1 - n0;
@@ -352,7 +364,7 @@ __global__ __launch_bounds__(64 * NW) void ep_few_down_kernel(
                 for (int i = 0; i < 4; ++i) q[i] = __builtin_amdgcn_readfirstlane(seg[g].pair[4 * a + i]);
                 const uint32_t p01 = c8 & 2 ? q[1] : q[0], p23 = c8 & 2 ? q[3] : q[2];
                 const uint32_t two = c8 & 4 ? p23 : p01, pair = c8 & 1 ? two >> 16 : two & 0xFFFFu;
-                hoff[a] = 8 * a + c8 < hrows ? (pair * 2 + part) * (uint32_t)s.I * 2 : kPast;
+                hoff[a] = 8 * a + c8 < hrows ? (pair * 2 + half) * (uint32_t)s.I * 2 : kPast;
             }
             if constexpr (F8) sb = buffer(downs + ((size_t)seg[g].expert * HB + n0 / 128) * KB, KB * 4);
         };
@@ -466,7 +478,7 @@ __global__ __launch_bounds__(64 * NW) void ep_few_down_kernel(
     __syncthreads();
     constexpr int TILE = NW * G * 32;   // f32x4 of 8 tokens: [wave][group of columns][quad][token]
     static_assert((TT + 1) / 2 * TILE * 16 <= NW * G * 2048, "they fit in the first two buffers");
-    if (part == 0)
+    if (half == 0)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
@@ -474,30 +486,85 @@ __global__ __launch_bounds__(64 * NW) void ep_few_down_kernel(
                 reinterpret_cast<f32x4 *>(t & 1 ? buf1 : buf0)[(t >> 1) * TILE + (wid * G + f) * 32 + quad * 8 + c8] =
                     acc[t][f];
     __syncthreads();
-    for (int i = threadIdx.x; i < TT * G * 32; i += 64 * NW) {
-        const int at = i % (G * 32), t = i / (G * 32), token = 8 * t + at % 8, col = n0 + at / 8 * 4;
-        if (token >= s.T || col >= s.H) continue;   // H % 8 == 0
+    const auto each = [&](const auto &f) {   // 4 columns of a token: f(their place in the sums, token, column)
+        for (int i = threadIdx.x; i < TT * G * 32; i += 64 * NW) {
+            const int at = i % (G * 32), t = i / (G * 32), token = 8 * t + at % 8, col = n0 + at / 8 * 4;
+            if (token < s.T && col < s.H) f(t, at, (size_t)token * s.H + col);   // H % 8 == 0
+        }
+    };
+    const auto sum_up = [&](int t, int at) {
         const f32x4 *sums = reinterpret_cast<const f32x4 *>(t & 1 ? buf1 : buf0) + (t >> 1) * TILE + at;
         f32x4 v = {};
 #pragma unroll
         for (int q = 0; q < NW; ++q) v += sums[q * G * 32];
-        const size_t o = (size_t)token * s.H + col;
+        return v;
+    };
+    const auto finish = [&](f32x4 v, size_t o) {
         if (residual) {
             const uint2 r = *reinterpret_cast<const uint2 *>(residual + o);
             v += f32x4{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
         }
         *reinterpret_cast<uint2 *>(y + o) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    };
+    if (parts == 1) {
+        each([&](int t, int at, size_t o) { finish(sum_up(t, at), o); });
+        return;
     }
+    // The block that is done last adds up the parts, in their order.  The parts
+    // go past the XCDs' own L2s by stores and loads of the whole chip's scope:
+    // fences would write back and drop those L2s (2 parts of a token's layer: 171
+    // us instead of 71).
+    const size_t plane = (size_t)s.T * s.H;
+    each([&](int t, int at, size_t o) {
+        const f32x4 v = sum_up(t, at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            __hip_atomic_store(partial + bp * plane + o + i, v[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    });
+    __builtin_amdgcn_s_waitcnt(0);   // they have arrived where every XCD sees them
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last_block = __hip_atomic_fetch_add(&arrived[ct], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
+    __syncthreads();
+    if (!last_block) return;
+    each([&](int, int, size_t o) {
+        f32x4 v = {};
+#pragma unroll 4
+        for (int q = 0; q < parts; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[i] += __hip_atomic_load(partial + q * plane + o + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        finish(v, o);
+    });
 }
 
+struct Work {   // the workspace's parts
+    int32_t *count, *arrived;
+    FewSegment *seg;
+    uint16_t *h;
+    float *partial;
+    Work(const FewShape &s, uint8_t *ws)
+        : count(reinterpret_cast<int32_t *>(ws)), arrived(count + 64), seg(reinterpret_cast<FewSegment *>(ws + kFewHead)),
+          h(reinterpret_cast<uint16_t *>(ws + few_h_offset(s))),
+          partial(reinterpret_cast<float *>(ws + few_partial_offset(s))) {}
+};
+
 template <bool F8, int RT, int TT>
-hipError_t launch_down(const FewShape &s, const int32_t *count, const FewSegment *seg, const uint16_t *h,
-                       const uint8_t *down, const float *downs, const uint16_t *residual, uint16_t *y,
-                       hipStream_t stream) {
-    constexpr int G = 2, NW = 8, NB = 4;
-    const int blocks = (s.H + 16 * G - 1) / (16 * G);
-    hipLaunchKernelGGL((ep_few_down_kernel<F8, RT, TT, G, NW, NB>), dim3((unsigned)blocks), dim3(64 * NW), 0, stream, s,
-                       count, seg, h, down, downs, residual, y);
+hipError_t launch_down(const FewShape &s, const Work &k, const uint8_t *down, const float *downs,
+                       const uint16_t *residual, uint16_t *y, hipStream_t stream) {
+    constexpr int G = kFewColumns / 16, NW = 8, NB = 4;
+    const int cols = few_columns(s), parts = few_parts(s);
+    hipLaunchKernelGGL((ep_few_down_kernel<F8, RT, TT, G, NW, NB>), dim3((unsigned)(cols * parts)), dim3(64 * NW), 0,
+                       stream, s, k.count, k.seg, k.h, down, downs, residual, y, cols, parts, k.partial, k.arrived);
+    return hipGetLastError();
+}
+
+template <bool F8, int GU, int MT, int NW>
+hipError_t launch_up(const FewShape &s, const Work &k, const uint16_t *x, const int64_t *idx, const float *w,
+                     const uint8_t *up, const float *ups, hipStream_t stream) {
+    const int cols = (s.I + 16 * GU - 1) / (16 * GU);
+    hipLaunchKernelGGL((ep_few_up_kernel<F8, GU, MT, NW, 2>), dim3((unsigned)(1 + (int64_t)s.T * s.k * cols)),
+                       dim3(64 * NW), 0, stream, s, x, idx, w, up, ups, k.count, k.seg, k.arrived, k.h, cols);
     return hipGetLastError();
 }
 
@@ -505,23 +572,14 @@ template <bool F8>
 hipError_t launch(const FewShape &s, const uint16_t *x, const int64_t *idx, const float *w, const uint8_t *up,
                   const float *ups, const uint8_t *down, const float *downs, const uint16_t *residual, uint16_t *y,
                   uint8_t *ws, hipStream_t stream) {
-    int32_t *count = reinterpret_cast<int32_t *>(ws);
-    FewSegment *seg = reinterpret_cast<FewSegment *>(ws + kFewHead);
-    uint16_t *h = reinterpret_cast<uint16_t *>(ws + few_h_offset(s));
-    const int cols = (s.I + 15) / 16;
-    const dim3 grid((unsigned)(1 + (int64_t)s.T * s.k * cols));
-    if (s.T <= 16)
-        hipLaunchKernelGGL((ep_few_up_kernel<F8, 1, 4, 2>), grid, dim3(256), 0, stream, s, x, idx, w, up, ups, count, seg,
-                           h, cols);
-    else
-        hipLaunchKernelGGL((ep_few_up_kernel<F8, 2, 4, 3>), grid, dim3(256), 0, stream, s, x, idx, w, up, ups, count, seg,
-                           h, cols);
-    const hipError_t e = hipGetLastError();
+    const Work k(s, ws);
+    const hipError_t e = s.T * s.k > 8 * s.E ? launch_up<F8, 2, 2, 4>(s, k, x, idx, w, up, ups, stream)
+                                             : launch_up<F8, 2, 1, 4>(s, k, x, idx, w, up, ups, stream);
     if (e != hipSuccess) return e;
-    if (s.T <= 8) return launch_down<F8, 1, 1>(s, count, seg, h, down, downs, residual, y, stream);
-    if (s.T <= 16) return launch_down<F8, 2, 2>(s, count, seg, h, down, downs, residual, y, stream);
-    if (s.T <= 32) return launch_down<F8, 2, 4>(s, count, seg, h, down, downs, residual, y, stream);
-    return launch_down<F8, 2, 8>(s, count, seg, h, down, downs, residual, y, stream);
+    if (s.T <= 8) return launch_down<F8, 1, 1>(s, k, down, downs, residual, y, stream);
+    if (s.T <= 16) return launch_down<F8, 2, 2>(s, k, down, downs, residual, y, stream);
+    if (s.T <= 32) return launch_down<F8, 2, 4>(s, k, down, downs, residual, y, stream);
+    return launch_down<F8, 2, 8>(s, k, down, downs, residual, y, stream);
 }
 
 }  // namespace

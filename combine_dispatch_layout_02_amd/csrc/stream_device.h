@@ -51,11 +51,21 @@ struct Step {
     __device__ __forceinline__ Step(const uint8_t *lds, uint32_t plo) {
         const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t *)lds + plo;
         vec16 v[G][2];
-        if constexpr (G == 2)
+        if constexpr (G == 4)
+            asm volatile(
+                "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\t"
+                "ds_read_b128 %2, %8 offset:2048\n\tds_read_b128 %3, %9 offset:2048\n\t"
+                "ds_read_b128 %4, %8 offset:4096\n\tds_read_b128 %5, %9 offset:4096\n\t"
+                "ds_read_b128 %6, %8 offset:6144\n\tds_read_b128 %7, %9 offset:6144\n\ts_waitcnt lgkmcnt(0)"
+                : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1]), "=&v"(v[2][0]), "=&v"(v[2][1]),
+                  "=&v"(v[3][0]), "=&v"(v[3][1])
+                : "v"(at), "v"(at ^ 64)
+                : "memory");
+        else if constexpr (G == 2)
             asm volatile(
                 "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\t"
                 "ds_read_b128 %2, %4 offset:2048\n\tds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
-                : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[G - 1][0]), "=&v"(v[G - 1][1])
+                : "=&v"(v[0][0]), "=&v"(v[0][1]), "=&v"(v[1][0]), "=&v"(v[1][1])
                 : "v"(at), "v"(at ^ 64)
                 : "memory");
         else
@@ -90,7 +100,7 @@ struct Stage {
     __device__ __forceinline__ void go(rsrc_t b0, rsrc_t b1, uint8_t *lds, uint32_t k, uint32_t bytes) const {
         const uint32_t past = k + piece < bytes ? 0u : kPast;   // the end of K
 #pragma unroll
-        for (int i = 0; i < 2 * G; ++i) load_to_lds(i < 2 ? b0 : b1, lds + i * 1024, (off[i] + piece) | past, k);
+        for (int i = 0; i < 2 * G; ++i) load_to_lds(i < G ? b0 : b1, lds + i * 1024, (off[i] + piece) | past, k);
     }
 };
 
