@@ -13,8 +13,8 @@
 // second, so a lane's 4 results lie at consecutive columns of one token.
 //
 // No expert's rows are gathered first: a block of the first kernel finds its
-// expert's tokens in topk_idx by itself, one lane to a token, and one extra
-// block writes down for the second kernel which expert has which rows.
+// expert and that one's tokens in topk_idx by itself, and one extra block writes
+// down for the second kernel which expert has which rows.
 #include "dense.h"
 #include "ep_device.h"
 #include "stream_device.h"
@@ -24,6 +24,17 @@ namespace ep {
 namespace {
 
 // ---------------------------------------------------------------- the segments
+
+// Sum up to and with the lane.
+__device__ __forceinline__ int scan(int v) {
+    const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
 
 // Which expert has which rows, for the second kernel: one block, experts
 // ascending, each one's tokens ascending, 16 a segment.  It also clears that
@@ -49,14 +60,6 @@ __device__ void make_plan(Plan &p, const FewShape &s, const int64_t *idx, int32_
         if (ok) atomicOr(&p.used[e >> 5], 1u << (e & 31));
     }
     __syncthreads();
-    const auto scan = [&](int v) {   // sum up to and with the lane
-#pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-            const int u = __shfl_up(v, d);
-            if (lane >= d) v += u;
-        }
-        return v;
-    };
     if (wid == 0) {
         const uint32_t a = p.used[2 * lane], b = p.used[2 * lane + 1];
         uint64_t bits = (uint64_t)b << 32 | a;
@@ -109,10 +112,20 @@ __device__ void make_plan(Plan &p, const FewShape &s, const int64_t *idx, int32_
 
 // ---------------------------------------------------------------- gate and up
 
+// The experts that are used and their tokens, 16 MT at a time, are numbered in
+// order; this is what a block needs to find its own: pairs of every expert.
+struct Census {
+    uint16_t ids[kFewTokens * 32];   // topk_idx, 0xFFFF where masked
+    uint32_t pairs[4096];
+};
+
 // One block: 16 GU columns of h (those gate and up rows of the weights) for up
-// to 16 MT tokens of one expert; NW waves, each with a part of K.  The
-// grid has a block column for every pair (t, j); the block whose pair is the
-// first of its expert's (or of the next 16 MT tokens of it) does the work.
+// to 16 MT tokens of one expert; NW waves, each with a part of K.  There are at
+// most T k such groups of tokens, and at most one for every expert and one more
+// for every 16 MT pairs: the grid has no more than that.  (A block for every
+// pair, all but the expert's first ending at once, kept their places busy for the
+// time of a look at topk_idx: the layer for 64 tokens, 96 experts, top-6, took 201
+// us instead of 175, for 32 tokens, 64 experts, top-8, 499 instead of 471.)
 template <bool F8, int GU, int MT, int NW, int NB>
 __global__ __launch_bounds__(64 * NW) void ep_few_up_kernel(
     FewShape s, const uint16_t *__restrict__ x, const int64_t *__restrict__ idx, const float *__restrict__ w,
@@ -133,34 +146,60 @@ __global__ __launch_bounds__(64 * NW) void ep_few_up_kernel(
         make_plan(*reinterpret_cast<Plan *>(buf0), s, idx, count, seg, arrived);
         return;
     }
-    const int p = (blockIdx.x - 1) / cols, n0 = (int)((blockIdx.x - 1) % cols) * 16 * GU;
-    const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int slot = (blockIdx.x - 1) / cols, n0 = (int)((blockIdx.x - 1) % cols) * 16 * GU;
+    const int tid = threadIdx.x, lane = tid & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int r16 = lane & 15, quad = lane >> 4;
 
+    static_assert(sizeof(Census) <= sizeof(buf0), "it uses the buffer");
+    Census &c = *reinterpret_cast<Census *>(buf0);
+    for (int i = tid; i < s.E; i += 64 * NW) c.pairs[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < s.T * s.k; i += 64 * NW) {
+        const int64_t id = idx[i];
+        const bool ok = id >= 0 && id < s.E;
+        c.ids[i] = ok ? (uint16_t)id : 0xFFFF;
+        if (ok) atomicAdd(&c.pairs[(int)id], 1u);
+    }
+    __syncthreads();
+    // every wave by itself: a run of experts for each lane
+    const auto groups = [&](int e) { return (int)((c.pairs[e] + 16 * MT - 1) / (16 * MT)); };
+    const int run = (s.E + kWave - 1) / kWave, e0 = min(lane * run, s.E), e1 = min(e0 + run, s.E);
+    int own = 0;
+    for (int i = e0; i < e1; ++i) own += groups(i);
+    int at = scan(own) - own, found = -1, group = 0;
+    if (slot >= at && slot < at + own)
+        for (int i = e0; i < e1; ++i) {
+            const int g = groups(i);
+            if (slot < at + g) {
+                found = i;
+                group = slot - at;
+                break;
+            }
+            at += g;
+        }
+    const uint64_t finder = __ballot(found >= 0);
+    if (finder == 0) return;   // no such group; the same for the whole block
+    const int e = __builtin_amdgcn_readlane(found, __builtin_ctzll(finder));
+    const int r0 = 16 * MT * __builtin_amdgcn_readlane(group, __builtin_ctzll(finder));
+
     // the expert's tokens, a lane for each
-    const int64_t e64 = idx[p];
-    if (e64 < 0 || e64 >= s.E) return;
-    const int e = __builtin_amdgcn_readfirstlane((int)e64);
     int j = -1;
     float wt = 0.0f;
     if (lane < s.T)
         for (int i = 0; i < s.k; ++i)
-            if (idx[lane * s.k + i] == e) {
+            if (c.ids[lane * s.k + i] == e) {
                 wt = j < 0 ? w[lane * s.k + i] : wt + w[lane * s.k + i];
                 j = j < 0 ? i : j;
             }
     const uint64_t has = __ballot(j >= 0);
     const int rank = __popcll(has & lanemask_lt());
-    const uint64_t mine = __ballot(j >= 0 && lane * s.k + j == p);
-    if (mine == 0) return;   // a token's second slot with the expert
-    const int r0 = __popcll(has & (mine - 1));
-    if (r0 % (16 * MT) != 0) return;
-    const int rows = min(16 * MT, __popcll(has) - r0);
+    const int rows = min(16 * MT, (int)__popcll(has) - r0);   // below 0 where the pairs were more than the tokens
+    if (rows <= 0) return;   // the same for the whole block
     if (wid == 0 && j >= 0 && rank >= r0 && rank < r0 + rows) {
         rows_pair[rank - r0] = lane * s.k + j;
         rows_w[rank - r0] = wt;
     }
-    __syncthreads();
+    __syncthreads();   // nobody reads the census any more
 
     const uint32_t kbytes = (uint32_t)s.H * (F8 ? 1 : 2);
     const int KU = (s.H + KE - 1) / KE;
@@ -562,8 +601,9 @@ hipError_t launch_down(const FewShape &s, const Work &k, const uint8_t *down, co
 template <bool F8, int GU, int MT, int NW>
 hipError_t launch_up(const FewShape &s, const Work &k, const uint16_t *x, const int64_t *idx, const float *w,
                      const uint8_t *up, const float *ups, hipStream_t stream) {
-    const int cols = (s.I + 16 * GU - 1) / (16 * GU);
-    hipLaunchKernelGGL((ep_few_up_kernel<F8, GU, MT, NW, 2>), dim3((unsigned)(1 + (int64_t)s.T * s.k * cols)),
+    const int cols = (s.I + 16 * GU - 1) / (16 * GU), pairs = s.T * s.k;
+    const int used = pairs < s.E ? pairs : s.E, most = used + pairs / (16 * MT), groups = most < pairs ? most : pairs;
+    hipLaunchKernelGGL((ep_few_up_kernel<F8, GU, MT, NW, 2>), dim3((unsigned)(1 + (int64_t)groups * cols)),
                        dim3(64 * NW), 0, stream, s, x, idx, w, up, ups, k.count, k.seg, k.arrived, k.h, cols);
     return hipGetLastError();
 }

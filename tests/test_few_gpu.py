@@ -71,7 +71,8 @@ def test_few(ep, size, fp8, masked, residual):
 
 
 @pytest.mark.parametrize("fp8", [True, False])
-@pytest.mark.parametrize("T,k,spread", [(64, 1, 1), (64, 8, 8), (40, 2, 2), (33, 4, 5), (17, 2, 1), (64, 32, 3)])
+@pytest.mark.parametrize("T,k,spread", [(64, 1, 1), (64, 8, 8), (40, 2, 2), (33, 4, 5), (17, 2, 1), (12, 2, 1),
+                                        (2, 32, 1), (9, 32, 1), (64, 32, 3)])
 def test_crowded(ep, T, k, spread, fp8):
     """Few experts for many tokens (several row tiles each), slots that name one expert again and again."""
     d = draw(T, 256, 128, 8, k, fp8, seed=5, masked=0.1, residual=True, spread=spread)
