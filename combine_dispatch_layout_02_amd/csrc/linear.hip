@@ -11,11 +11,12 @@
 // read from there in the matrix instruction's layout, the second through the
 // transposing LDS read.  Q is the instruction's first operand, R its second, so
 // a lane's 4 results lie at consecutive c.
+#include <type_traits>
+
 #include "dense.h"
 #include "ep_device.h"
 #include "stream_device.h"
 #include "tile_device.h"
-#include "tile_order.h"
 
 namespace ep {
 namespace {
@@ -78,7 +79,7 @@ struct Const {
     static constexpr int value = V;
 };
 template <typename F>
-__device__ __forceinline__ void with_activation(int act, const F &f) {
+__host__ __device__ __forceinline__ void with_activation(int act, const F &f) {
     switch (act) {
         case kActRelu: return f(Const<kActRelu>());
         case kActSilu: return f(Const<kActSilu>());
@@ -139,7 +140,7 @@ struct Side {
     static __device__ __forceinline__ int place(int row) { return KS == 64 ? row & 7 : (4 - (row >> 2)) & 3; }
     // The line in place s (s % BLOCKS: the load, s / BLOCKS: where in it): 0-3, 8-11, 4-7, 12-15, 16-19, ...
     static __device__ __forceinline__ int line(int s) { return (s & 0x33) | (s & 4) << 1 | (s & 8) >> 1; }
-    static constexpr int line_at(int s) { return s % BLOCKS * PLACE + s / BLOCKS * LINE; }
+    static __host__ __device__ constexpr int line_at(int s) { return s % BLOCKS * PLACE + s / BLOCKS * LINE; }
 
     // first: the tile's first row, row: the wave's first row in the tile
     __device__ __forceinline__ void init(const Operand &o, int64_t first, int row, int lane, int wid) {
@@ -169,7 +170,8 @@ struct Side {
                 off[i] = (uint32_t)(kfirst[i] * o.ld * 2) + min(lane * 16 % LINE / 16, last) * 16;
             }
             // lane i of 16 names line i / 4 and its columns 4 (i % 4) .. + 3, and gets column i of the 4 lines
-            from = (uint32_t)(((r16 >> 2) + 4 * (quad & 1)) * PLACE + (quad >> 1) * line_at(16) + (row + (r16 & 3) * 4) * 2);
+            const int s = (r16 >> 2) + 4 * (quad & 1);
+            from = (uint32_t)(line_at(s) + (quad >> 1) * line_at(16) + (row + (r16 & 3) * 4) * 2);
         }
     }
     // from: the step's first element, left: of the sum's length from there on
@@ -258,90 +260,129 @@ __device__ __forceinline__ void finish(const Product &p, int64_t r, int64_t c, E
     v.store(p.out, p.out_f32, at);
 }
 
-// One block: BR rows by BC columns of C, WR by WC waves; a step is KS of k. NB
+// Which tile a block takes.  Consecutive blocks go to the 8 XCDs in turn; each
+// XCD takes an eighth of the tiles, in groups of 8 rows by 4 columns (fewer rows
+// where there are fewer), which share their operands in its L2.
+struct Order {
+    int rows, cols;
+    __host__ __device__ int64_t blocks() const { return ((int64_t)rows * cols + 7) / 8 * 8; }
+    __device__ __forceinline__ bool tile(uint32_t block, int *row, int *col) const {
+        const uint32_t total = rows * cols, share = (total + 7) / 8, t = block % 8 * share + block / 8;
+        if (t >= total) return false;
+        const uint32_t band = t / (8 * cols), in = t % (8 * cols), left = rows - 8 * band, high = left < 8 ? left : 8;
+        const uint32_t group = in / (4 * high), at = in % (4 * high), wide = cols - 4 * group < 4 ? cols - 4 * group : 4;
+        *row = (int)(8 * band + at / wide);
+        *col = (int)(4 * group + at % wide);
+        return true;
+    }
+};
+
+// One block: BR rows by BC columns of C, WR by WC waves; a step is KS of k.  NB
 // steps' operands have room in LDS: while step s is multiplied, the fragments of
 // s + 1 are read and the operands of s + NB are on their way into the place of s,
-// which every wave had read before the barrier.
-template <bool TR, bool TQ, int BR, int BC, int WR, int WC, int KS, int NB>
-__global__ __launch_bounds__(64 * WR * WC) void ep_linear_tile_kernel(Product p) {
-    constexpr int W = WR * WC, NR = BR / WR / 16, NC = BC / WC / 16, CH = KS / 32;
+// which every wave had read before the barrier.  Where tiles are few, SK such
+// groups of waves each take a part of the steps, and the first adds up the sums
+// in order.
+template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK>
+struct Tile {
+    static constexpr int W = WR * WC, THREADS = 64 * W * SK, NR = BR / WR / 16, NC = BC / WC / 16, CH = KS / 32;
+    static_assert(NC % (GATED ? 4 : 2) == 0, "pairs of groups of columns, of a gate's and of their factors, in one wave");
+    static_assert(NB >= 2 && NB <= 4, "as many buffers");
     typedef Side<TR, BR, W, KS> R;
     typedef Side<TQ, BC, W, KS> Q;
-    constexpr int BYTES = R::BYTES + Q::BYTES;
-    static_assert(NC % 4 == 0, "pairs of groups of a gate's columns and of their factors in one wave");
-    static_assert(NB >= 3 && NB <= 5, "as many buffers");
-    __shared__ __attribute__((aligned(16))) uint8_t buf0[BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t buf1[BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t buf2[BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t buf3[NB > 3 ? BYTES : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t buf4[NB > 4 ? BYTES : 16];
+    static constexpr int BYTES = R::BYTES + Q::BYTES;
+    static_assert(SK == 1 || (W * NC * NR * 1024 <= SK * BYTES && SK <= NB + 1), "a buffer takes the sums of a part");
+    static __device__ __forceinline__ void run(const Product &p, uint32_t block);
+};
+
+template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK>
+__device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK>::run(const Product &p, uint32_t block) {
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[SK * BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[SK * BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[NB > 2 ? SK * BYTES : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t buf3[NB > 3 ? SK * BYTES : 16];
+    const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int wid = wave % W, sk = wave / W;
     const auto buf = [&](int j) {
-        return j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : (j % NB == 2 ? buf2 : (j % NB == 3 ? buf3 : buf4)));
+        return (j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : (j % NB == 2 ? buf2 : buf3))) + sk * BYTES;
     };
 
     int rt, ct;
-    if (!TileOrder{p.rtiles, p.ctiles}.tile(blockIdx.x, &rt, &ct)) return;
-    const int lane = threadIdx.x & (kWave - 1), wid = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    if (!Order{p.rtiles, p.ctiles}.tile(block, &rt, &ct)) return;
     const int wr = wid / WC, wc = wid % WC;
-    const int64_t r0 = (int64_t)rt * BR, c0 = (int64_t)ct * (p.gated ? BC / 2 : BC);
+    const int64_t r0 = (int64_t)rt * BR, c0 = (int64_t)ct * (GATED ? BC / 2 : BC);
 
-    // the wave's columns: half of them from each half of the tile
-    const int cw = wc * (BC / 2 / WC);
-    const auto qrow = [](int f) { return (f / (NC / 2)) * (BC / 2) + f % (NC / 2) * 16; };
+    // the wave's groups of 16 columns; gated: half of them from each half of the tile
+    const int cw = wc * (GATED ? BC / 2 / WC : BC / WC);
+    const auto qrow = [](int f) { return GATED ? (f / (NC / 2)) * (BC / 2) + f % (NC / 2) * 16 : f * 16; };
     R lr;
     Q lq;
     lr.init(p.r, r0, wr * (BR / WR), lane, wid);
     lq.init(p.q, c0, cw, lane, wid);
     constexpr int L = R::NL + Q::NL;
-    const int steps = (int)((p.k + KS - 1) / KS), all = steps * p.parts;
-    // the steps are staged in turn: where the next one starts
-    const uint16_t *rp = lr.base, *qp = lq.base;
-    int at = 0, part = 0;
+    const int k = (int)p.k, steps = (k + KS - 1) / KS, all = steps * p.parts;
+    // this group's steps: as many for each (barriers), the last one's may lie past the sum
+    const int share = (all + SK - 1) / SK, s0 = sk * share;
+    // The steps are staged in turn: where the next one starts, what is left of k
+    // there (0 past the group's last step: nothing is read).
+    int part = s0 / steps, at = s0 % steps, todo = min(share, all - s0), left = todo > 0 ? k - at * KS : 0;
+    const uint16_t *rp = lr.base + part * p.part + at * lr.step, *qp = lq.base + at * lq.step;
     const auto advance = [&]() {
         rp += lr.step;
         qp += lq.step;
+        left -= KS;
         if (++at == steps) {
             at = 0;
             rp = lr.base + ++part * p.part;
             qp = lq.base;
+            left = k;
         }
+        if (--todo <= 0) left = 0;
     };
     const auto stage = [&](uint8_t *to, int i) {   // load i of the wave
-        const int left = part < p.parts ? (int)min(p.k - (int64_t)at * KS, (int64_t)KS) : 0;
         if (i < R::NL)
             lr.load(to, i, wid, rp, left);
         else
             lq.load(to + R::BYTES, i - R::NL, wid, qp, left);
         if (i == L - 1) advance();
     };
-    struct Fragments {
-        bf16x8 r[CH][NR], q[CH][NC];
+    struct Fragments {   // of 32 of k
+        bf16x8 r[NR], q[NC];
     };
-    const auto read = [&](const uint8_t *from, Fragments &f, int i) {   // fragment i of a step
-        const int c = i / (NR + NC), j = i % (NR + NC);
-        if (j < NC)
-            f.q[c][j] = lq.fragment(from + R::BYTES, qrow(j), c);
+    const auto read = [&](const uint8_t *from, Fragments &f, int c, int i) {   // fragment i of part c of a step
+        if (i < NC)
+            f.q[i] = lq.fragment(from + R::BYTES, qrow(i), c);
         else
-            f.r[c][j - NC] = lr.fragment(from, 16 * (j - NC), c);
+            f.r[i - NC] = lr.fragment(from, 16 * (i - NC), c);
     };
 
     f32x4 acc[NC][NR] = {};
-    const auto step = [&](const Fragments &f, Fragments &next, uint8_t *mine, const uint8_t *after) {
-        // the next step's operands have arrived (behind them NB - 2 steps' are
-        // under way), and this step's fragments: every wave's after the barrier
-        __builtin_amdgcn_s_waitcnt(0x0070 | ((NB - 2) * L & 15) | ((NB - 2) * L >> 4) << 14);   // lgkmcnt(0) too
-        barrier_only();
-        constexpr int READS = CH * (NR + NC), GROUPS = CH * NR;
+    const auto step = [&](Fragments (&f)[2], int first, uint8_t *mine, const uint8_t *after) {
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {   // NC matrix instructions, and a share of the rest
+        for (int c = 0; c < CH; ++c) {
+            const Fragments &now = f[(first + c) % 2];
+            Fragments &next = f[(first + c + 1) % 2];
+            const bool last = c == CH - 1;
+            if (last) {
+                // the next step's operands have arrived (behind them NB - 2 steps' are
+                // under way), and the last of this step's fragments: every wave's after
+                // the barrier, and this step's place is free
+                __builtin_amdgcn_s_waitcnt(0x0070 | ((NB - 2) * L & 15) | ((NB - 2) * L >> 4) << 14);   // lgkmcnt(0) too
+                barrier_only();
+            }
+            constexpr int READS = NR + NC;
 #pragma unroll
-            for (int i = g * L / GROUPS; i < (g + 1) * L / GROUPS; ++i) stage(mine, i);
+            for (int m = 0; m < NR; ++m) {   // NC matrix instructions, and a share of the rest
+                if (last)
 #pragma unroll
-            for (int i = g * READS / GROUPS; i < (g + 1) * READS / GROUPS; ++i) read(after, next, i);
-            const int c = g / NR, m = g % NR;
+                    for (int i = m * L / NR; i < (m + 1) * L / NR; ++i) stage(mine, i);
 #pragma unroll
-            for (int n = 0; n < NC; ++n) acc[n][m] = mfma(f.q[c][n], f.r[c][m], acc[n][m]);
-            __builtin_amdgcn_sched_barrier(0);
+                for (int i = m * READS / NR; i < (m + 1) * READS / NR; ++i)
+                    read(last ? after : mine, next, last ? 0 : c + 1, i);
+#pragma unroll
+                for (int n = 0; n < NC; ++n) acc[n][m] = mfma(now.q[n], now.r[m], acc[n][m]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
         }
     };
 #pragma unroll
@@ -352,58 +393,82 @@ __global__ __launch_bounds__(64 * WR * WC) void ep_linear_tile_kernel(Product p)
     barrier_only();
     Fragments f[2];
 #pragma unroll
-    for (int i = 0; i < CH * (NR + NC); ++i) read(buf0, f[0], i);
+    for (int i = 0; i < NR + NC; ++i) read(buf(0), f[0], 0, i);
     constexpr int TURN = NB % 2 ? 2 * NB : NB;
     // whole turns: steps past the last one multiply zeros
-    for (int s = 0; s < all; s += TURN)
+    for (int s = 0; s < share; s += TURN)
 #pragma unroll
-        for (int j = 0; j < TURN; ++j) step(f[j % 2], f[(j + 1) % 2], buf(j), buf(j + 1));
+        for (int j = 0; j < TURN; ++j) step(f, j * CH % 2, buf(j), buf(j + 1));
     wait_loads<0>();
 
+    if constexpr (SK > 1) {
+        __syncthreads();
+        const auto sums = [&](int q) {   // of part q > 0, this wave's
+            return reinterpret_cast<f32x4 *>(q == 1 ? buf0 : (q == 2 ? buf1 : (q == 3 ? buf2 : buf3))) +
+                   wid * NC * NR * kWave + lane;
+        };
+#pragma unroll
+        for (int q = 1; q < SK; ++q)
+            if (sk == q)
+#pragma unroll
+                for (int i = 0; i < NC * NR; ++i) sums(q)[i * kWave] = acc[i / NR][i % NR];
+        __syncthreads();
+        if (sk > 0) return;
+#pragma unroll
+        for (int q = 1; q < SK; ++q)
+#pragma unroll
+            for (int i = 0; i < NC * NR; ++i) acc[i / NR][i % NR] += sums(q)[i * kWave];
+    }
+
     // pairs of groups of columns; the residual's values are all on their way before the first is used
-    const int r16 = lane & 15, quad = lane >> 4, column = cw + Eight::column(quad);
-    constexpr int PAIRS = NC / 2;
-    vec16 residual[PAIRS][NR] = {};
+    const int r16 = lane & 15, quad = lane >> 4;
+    constexpr int PAIRS = GATED ? NC / 4 : NC / 2, HALF = GATED ? NC / 2 : 0;   // without a gate the factors are not looked at
     const auto row = [&](int m) { return r0 + wr * (BR / WR) + 16 * m + r16; };
-    const auto inside = [&](int f, int m) {
-        return row(m) < p.r.rows && c0 + column + qrow(2 * f) < p.out_ld && (!p.gated || f < PAIRS / 2);
-    };
+    const auto column = [&](int f) { return c0 + cw + 32 * f + Eight::column(quad); };
+    const auto inside = [&](int f, int m) { return row(m) < p.r.rows && column(f) < p.out_ld; };
+    vec16 residual[PAIRS][NR] = {};
     if (p.residual)
 #pragma unroll
         for (int f = 0; f < PAIRS; ++f)
 #pragma unroll
             for (int m = 0; m < NR; ++m)
-                if (inside(f, m)) residual[f][m] = ld16(p.residual + row(m) * p.out_ld + c0 + column + qrow(2 * f));
+                if (inside(f, m)) residual[f][m] = ld16(p.residual + row(m) * p.out_ld + column(f));
 #pragma unroll
     for (int f = 0; f < PAIRS; ++f) {
-        if (p.gated && f >= PAIRS / 2) break;
 #pragma unroll
         for (int m = 0; m < NR; ++m) {
-            const Eight v(acc[2 * f][m], acc[2 * f + 1][m]);
-            constexpr int HALF = NC / 2;
-            const Eight u(acc[(2 * f + HALF) % NC][m], acc[(2 * f + 1 + HALF) % NC][m]);
-            if (inside(f, m)) finish(p, row(m), c0 + column + qrow(2 * f), v, u, residual[f][m]);
+            const Eight v(acc[2 * f][m], acc[2 * f + 1][m]), u(acc[2 * f + HALF][m], acc[2 * f + 1 + HALF][m]);
+            if (inside(f, m)) finish(p, row(m), column(f), v, u, residual[f][m]);
         }
     }
 }
 
-template <bool TR, bool TQ, int BR, int BC, int WR, int WC, int KS, int NB>
+template <typename T>
+__global__ __launch_bounds__(T::THREADS) void ep_linear_tile_kernel(Product p) {
+    T::run(p, blockIdx.x);
+}
+
+template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK = 1>
 hipError_t launch_tile(Product p, hipStream_t stream) {
-    const int cols = p.gated ? BC / 2 : BC;
+    typedef Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK> T;
+    const int cols = GATED ? BC / 2 : BC;
     p.rtiles = (int)((p.r.rows + BR - 1) / BR);
     p.ctiles = (int)((p.out_ld + cols - 1) / cols);
-    hipLaunchKernelGGL((ep_linear_tile_kernel<TR, TQ, BR, BC, WR, WC, KS, NB>),
-                       dim3((unsigned)TileOrder::blocks(p.rtiles, p.ctiles)), dim3(64 * WR * WC), 0, stream, p);
+    hipLaunchKernelGGL(ep_linear_tile_kernel<T>, dim3((unsigned)Order{p.rtiles, p.ctiles}.blocks()), dim3(T::THREADS), 0,
+                       stream, p);
     return hipGetLastError();
 }
 
-template <bool TR, bool TQ>
+template <bool TR, bool TQ, bool GATED>
 hipError_t launch_product(const Product &p, hipStream_t stream) {
-    const int64_t cols = p.gated ? 2 * p.out_ld : p.out_ld;
+    const int64_t cols = GATED ? 2 * p.out_ld : p.out_ld;
     const auto tiles = [&](int BR, int BC) { return ((p.r.rows + BR - 1) / BR) * ((cols + BC - 1) / BC); };
-    if (tiles(256, 256) >= 160) return launch_tile<TR, TQ, 256, 256, 2, 4, 32, 4>(p, stream);
-    if (tiles(128, 128) >= 160) return launch_tile<TR, TQ, 128, 128, 2, 2, 32, 4>(p, stream);
-    return launch_tile<TR, TQ, 64, 64, 4, 1, 64, 4>(p, stream);
+    if (tiles(256, 256) >= 160) return launch_tile<TR, TQ, GATED, 256, 256, 2, 4, 32, 4>(p, stream);
+    if (tiles(128, 128) >= 160) return launch_tile<TR, TQ, GATED, 128, 128, 2, 2, 32, 4>(p, stream);
+    if (tiles(64, 128) >= 160) return launch_tile<TR, TQ, GATED, 64, 128, 2, 2, 64, 4>(p, stream);
+    if (tiles(64, 64) <= 256 && p.k * p.parts >= 512)
+        return launch_tile<TR, TQ, GATED, 64, 64, 4, 1, 32, 4, 4>(p, stream);
+    return launch_tile<TR, TQ, GATED, 64, 64, 4, 1, 64, 4>(p, stream);
 }
 
 // ---------------------------------------------------------------- few rows
@@ -558,24 +623,26 @@ hipError_t launch_stream(const Product &p, hipStream_t stream) {
 
 // dz from dy and z in bf16 (in one part, or in three: the rounded value, its
 // rounded rest and the rest of that, together the binary32 value) and the sums of
-// its columns over runs of kDzRows rows, for the bias.  A wave's lanes take 8
-// columns each, its 4 waves rows in turn, 4 at a time so that their loads are
-// under way together.
+// its columns over runs of kDzRows rows, for the bias.  A thread takes 8 columns
+// of a row, CG of them (a power of two, 64 at most) a row of up to 512 columns,
+// the block's others further rows, 4 at a time so that their loads are under way
+// together.
 constexpr int kDzThreads = 256;
-template <typename Dy>
+// A kernel for each activation: with all of them in one its code alone took a
+// small call 10 us to fetch (100 rows of 512: 18 us).
+template <typename Dy, int ACT, bool GATED>
 __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s, const Dy *__restrict__ dy,
                                                                   const uint16_t *__restrict__ z,
                                                                   uint16_t *__restrict__ dz, int parts,
-                                                                  float *__restrict__ sums) {
-    constexpr int W = kDzThreads / kWave, D = sizeof(Dy) / 2, AT_ONCE = 4;
-    static_assert(kDzRows % (W * AT_ONCE) == 0, "whole turns");
-    __shared__ float part[W][2][8][kWave];
-    const int lane = threadIdx.x & (kWave - 1), wid = threadIdx.x / kWave;
+                                                                  float *__restrict__ sums, int shift) {
+    constexpr int D = sizeof(Dy) / 2, AT_ONCE = 4;
+    __shared__ float part[2][8][kDzThreads];
+    const int sub = threadIdx.x >> shift, cg = threadIdx.x & ((1 << shift) - 1), rows = kDzThreads >> shift;
     const int cols = (s.N + 511) / 512, ct = blockIdx.x % cols;
-    const int64_t run = blockIdx.x / cols;
-    const int c = (ct * kWave + lane) * 8, wide = s.wide();
+    const int64_t run = blockIdx.x / cols, end = min((run + 1) * kDzRows, s.M);
+    const int c = ct * 512 + cg * 8, wide = s.wide();
     const int64_t plane = s.M * wide;
-    const bool kept = s.act != kActNone || s.gated;
+    constexpr bool KEPT = ACT != kActNone || GATED;
     float sum[2][8] = {};
     const auto unpack = [](vec16 v, float (&f)[8]) {
 #pragma unroll
@@ -600,21 +667,21 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
             st16(dz + n * plane + at, out);
         }
     };
-    for (int i0 = 0; i0 < kDzRows; i0 += W * AT_ONCE) {
+    for (int64_t r0 = run * kDzRows + sub; r0 < end; r0 += rows * AT_ONCE) {
         vec16 gv[AT_ONCE][D] = {}, zv[AT_ONCE] = {}, uv[AT_ONCE] = {};
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            const int64_t r = run * kDzRows + i0 + i * W + wid;
-            if (r >= s.M || c >= s.N) continue;
+            const int64_t r = r0 + i * rows;
+            if (r >= end || c >= s.N) continue;
 #pragma unroll
             for (int j = 0; j < D; ++j) gv[i][j] = ld16(dy + r * s.N + c + 8 / D * j);
-            if (kept) zv[i] = ld16(z + r * wide + c);
-            if (s.gated) uv[i] = ld16(z + r * wide + s.N + c);
+            if (KEPT) zv[i] = ld16(z + r * wide + c);
+            if (GATED) uv[i] = ld16(z + r * wide + s.N + c);
         }
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
-            const int64_t r = run * kDzRows + i0 + i * W + wid;
-            if (r >= s.M || c >= s.N) continue;
+            const int64_t r = r0 + i * rows;
+            if (r >= end || c >= s.N) continue;
             float g[8], a[8], b[8] = {}, v[8], u[8];
             if constexpr (D == 2) {
 #pragma unroll
@@ -624,34 +691,31 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
             }
             unpack(zv[i], v);
             unpack(uv[i], u);
-            with_activation(s.act, [&](auto act) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float f, d;
-                    derive<decltype(act)::value>(v[j], &f, &d);
-                    a[j] = s.gated ? g[j] * u[j] * d : g[j] * d;
-                    if (s.gated) b[j] = g[j] * f;
-                }
-            });
+            for (int j = 0; j < 8; ++j) {
+                float f, d;
+                derive<ACT>(v[j], &f, &d);
+                a[j] = GATED ? g[j] * u[j] * d : g[j] * d;
+                if (GATED) b[j] = g[j] * f;
+            }
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[0][j] += a[j], sum[1][j] += b[j];
             store(r * wide + c, a);
-            if (s.gated) store(r * wide + s.N + c, b);
+            if (GATED) store(r * wide + s.N + c, b);
         }
     }
     if (!sums) return;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < (GATED ? 2 : 1); ++h)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) part[wid][h][j][lane] = sum[h][j];
+        for (int j = 0; j < 8; ++j) part[h][j][threadIdx.x] = sum[h][j];
     __syncthreads();
-    if (wid > 1 || (wid == 1 && !s.gated) || c >= s.N) return;
+    if (sub > (GATED ? 1 : 0) || c >= s.N) return;   // the rows' threads, in order; rows is 4 or more
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         float v = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) v += part[w][wid][j][lane];
-        sums[run * wide + wid * s.N + c + j] = v;
+        for (int i = 0; i < rows; ++i) v += part[sub][j][(i << shift) + cg];
+        sums[run * wide + sub * s.N + c + j] = v;
     }
 }
 
@@ -699,7 +763,7 @@ hipError_t launch_linear(const LinearShape &s, const uint16_t *x, const uint16_t
     if (s.M <= 16) return s.gated ? launch_stream<true, 1>(p, stream) : launch_stream<false, 1>(p, stream);
     if (s.M <= 32) return s.gated ? launch_stream<true, 2>(p, stream) : launch_stream<false, 2>(p, stream);
     if (s.M <= 64) return s.gated ? launch_stream<true, 4>(p, stream) : launch_stream<false, 4>(p, stream);
-    return launch_product<false, false>(p, stream);
+    return s.gated ? launch_product<false, false, true>(p, stream) : launch_product<false, false, false>(p, stream);
 }
 
 hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const uint16_t *x, const uint16_t *w,
@@ -724,12 +788,21 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
     const int64_t runs = (s.M + kDzRows - 1) / kDzRows;
     if (grad_bias || (parts > 0 && (grad_x || grad_w))) {
         const dim3 grid((unsigned)(runs * ((s.N + 511) / 512)));
+        int shift = 0;   // threads to a row
+        while (shift < 6 && (8 << shift) < s.N) ++shift;
+        const auto launch = [&](const auto *from, auto gated) {
+            typedef std::remove_const_t<std::remove_pointer_t<decltype(from)>> Dy;
+            with_activation(s.act, [&](auto act) {
+                hipLaunchKernelGGL((ep_linear_dz_kernel<Dy, decltype(act)::value, decltype(gated)::value != 0>), grid,
+                                   dim3(kDzThreads), 0, stream, s, from, z, dz, parts, grad_bias ? sums : nullptr,
+                                   shift);
+            });
+        };
         if (s.f32)
-            hipLaunchKernelGGL(ep_linear_dz_kernel<float>, grid, dim3(kDzThreads), 0, stream, s,
-                               static_cast<const float *>(dy), z, dz, parts, grad_bias ? sums : nullptr);
+            s.gated ? launch(static_cast<const float *>(dy), Const<1>()) : launch(static_cast<const float *>(dy), Const<0>());
         else
-            hipLaunchKernelGGL(ep_linear_dz_kernel<uint16_t>, grid, dim3(kDzThreads), 0, stream, s,
-                               static_cast<const uint16_t *>(dy), z, dz, parts, grad_bias ? sums : nullptr);
+            s.gated ? launch(static_cast<const uint16_t *>(dy), Const<1>())
+                    : launch(static_cast<const uint16_t *>(dy), Const<0>());
     }
     if (grad_bias)
         hipLaunchKernelGGL(ep_linear_bias_kernel, dim3((unsigned)((wide + 15) / 16)), dim3(256), 0, stream, sums,
@@ -745,7 +818,7 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
         p.parts = 1;
         p.out_ld = s.K;
         p.out = grad_x;
-        e = launch_product<false, true>(p, stream);
+        e = launch_product<false, true, false>(p, stream);
         if (e != hipSuccess) return e;
     }
     if (grad_w) {
@@ -758,7 +831,7 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
         p.out_ld = s.K;
         p.out = grad_w;
         p.out_f32 = s.w32;
-        e = launch_product<true, true>(p, stream);
+        e = launch_product<true, true, false>(p, stream);
     }
     return e;
 }
