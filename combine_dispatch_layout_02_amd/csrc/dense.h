@@ -72,14 +72,20 @@ struct LinearShape {
 
 // Workspace of the backward pass: dz in bf16 (in three parts for an fp32
 // gradient of the weights) unless it is dy itself, the bias' sums of runs of rows.
-constexpr int kDzRows = 32;   // rows of a run
+// Rows of a run, by 512 columns for a block: 64, or fewer (4 at least) where the
+// blocks would not fill the chip (100 rows of 512: 64 rows 15 us, 4 rows 5).
+inline int dz_rows(const LinearShape &s) {
+    int r = 64;
+    while (r > 4 && (s.M + r - 1) / r * ((s.N + 511) / 512) < 1024) r /= 2;
+    return r;
+}
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 inline int dz_parts(const LinearShape &s) { return s.plain() ? 0 : (s.w32 ? 3 : 1); }
 inline size_t linear_sums_offset(const LinearShape &s) {
     return align256((size_t)dz_parts(s) * s.M * s.wide() * 2);
 }
 inline size_t linear_workspace(const LinearShape &s) {
-    return linear_sums_offset(s) + (size_t)((s.M + kDzRows - 1) / kDzRows) * s.wide() * 4;
+    return linear_sums_offset(s) + (size_t)((s.M + dz_rows(s) - 1) / dz_rows(s)) * s.wide() * 4;
 }
 
 hipError_t launch_linear(const LinearShape &s, const uint16_t *x, const uint16_t *w, const float *bias,

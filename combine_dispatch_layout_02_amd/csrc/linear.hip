@@ -459,15 +459,29 @@ hipError_t launch_tile(Product p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+int64_t tile_count(const Product &p, int BR, int BC) {
+    const int64_t cols = p.gated ? 2 * p.out_ld : p.out_ld;
+    return (p.r.rows + BR - 1) / BR * ((cols + BC - 1) / BC);
+}
+
+// The largest tile that still gives 160 blocks (of 256 CUs), as a larger one reads
+// less of LDS and memory for a product: with us at both sides
+//   4096 rows 7168 -> 2048 x 2   256 x 256 tiles 189, 128 x 128 276
+//   4096 rows 2048 -> 7168       256 x 256       133, 128 x 128 137
+//   1024 rows 7168 -> 2048       64 x 128 (256 tiles) 37.5, 128 x 128 (128) 62, 64 x 64 (512) 46
+//   512 rows 4096 -> 4096        64 x 128 (256) 24.0, 128 x 128 (128) 37.6, 64 x 64 (512) 27.5
+// and where even those of 64 x 64 are 128 at most, two groups of waves with half
+// the steps each, if those are 16 or more:
+//   64 rows 7168 -> 2048 x 2 27.9, halved 24.3;  100 rows 4096 -> 4096 18.1, 16.1
+//   300 rows 4096 -> 1024    17.8, halved 15.5;  512 rows 7168 -> 256  28.6, 24.9
 template <bool TR, bool TQ, bool GATED>
 hipError_t launch_product(const Product &p, hipStream_t stream) {
-    const int64_t cols = GATED ? 2 * p.out_ld : p.out_ld;
-    const auto tiles = [&](int BR, int BC) { return ((p.r.rows + BR - 1) / BR) * ((cols + BC - 1) / BC); };
+    const auto tiles = [&](int BR, int BC) { return tile_count(p, BR, BC); };
     if (tiles(256, 256) >= 160) return launch_tile<TR, TQ, GATED, 256, 256, 2, 4, 32, 4>(p, stream);
     if (tiles(128, 128) >= 160) return launch_tile<TR, TQ, GATED, 128, 128, 2, 2, 32, 4>(p, stream);
     if (tiles(64, 128) >= 160) return launch_tile<TR, TQ, GATED, 64, 128, 2, 2, 64, 4>(p, stream);
-    if (tiles(64, 64) <= 256 && p.k * p.parts >= 512)
-        return launch_tile<TR, TQ, GATED, 64, 64, 4, 1, 32, 4, 4>(p, stream);
+    if (tiles(64, 64) <= 128 && p.k * p.parts >= 1024)
+        return launch_tile<TR, TQ, GATED, 64, 64, 4, 1, 64, 4, 2>(p, stream);
     return launch_tile<TR, TQ, GATED, 64, 64, 4, 1, 64, 4>(p, stream);
 }
 
@@ -613,9 +627,14 @@ hipError_t launch_stream(const Product &p, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// 16 weight rows a block while every one has a CU of its own, else 32 and half the
+// waves (x 1 or 16 rows; 16 / 32 weight rows a block, us):
+//   7168 -> 1024  11.6 / 12.4     2048 -> 7168     11.8 / 6.7
+//   4096 -> 4096   9.0 / 9.1      7168 -> 7168     26.3 / 17.8
+//   7168 -> 2048 x 2, 1 row  12.9 / 11.9           4096 -> 16384  34.3 / 25.3
 template <bool GATED, int MT>
 hipError_t launch_stream(const Product &p, hipStream_t stream) {
-    if ((GATED ? 2 : 1) * p.out_ld >= 32 * 256) return launch_stream<GATED, 2, MT, 8, 2>(p, stream);
+    if ((GATED ? 2 : 1) * p.out_ld > 16 * 256) return launch_stream<GATED, 2, MT, 8, 2>(p, stream);
     return launch_stream<GATED, 1, MT, 16, 4>(p, stream);
 }
 
@@ -623,7 +642,7 @@ hipError_t launch_stream(const Product &p, hipStream_t stream) {
 
 // dz from dy and z in bf16 (in one part, or in three: the rounded value, its
 // rounded rest and the rest of that, together the binary32 value) and the sums of
-// its columns over runs of kDzRows rows, for the bias.  A thread takes 8 columns
+// its columns over runs of dz_rows rows, for the bias.  A thread takes 8 columns
 // of a row, CG of them (a power of two, 64 at most) a row of up to 512 columns,
 // the block's others further rows, 4 at a time so that their loads are under way
 // together.
@@ -634,12 +653,12 @@ template <typename Dy, int ACT, bool GATED>
 __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s, const Dy *__restrict__ dy,
                                                                   const uint16_t *__restrict__ z,
                                                                   uint16_t *__restrict__ dz, int parts,
-                                                                  float *__restrict__ sums, int shift) {
+                                                                  float *__restrict__ sums, int shift, int run_rows) {
     constexpr int D = sizeof(Dy) / 2, AT_ONCE = 4;
     __shared__ float part[2][8][kDzThreads];
     const int sub = threadIdx.x >> shift, cg = threadIdx.x & ((1 << shift) - 1), rows = kDzThreads >> shift;
     const int cols = (s.N + 511) / 512, ct = blockIdx.x % cols;
-    const int64_t run = blockIdx.x / cols, end = min((run + 1) * kDzRows, s.M);
+    const int64_t run = blockIdx.x / cols, end = min((run + 1) * run_rows, s.M);
     const int c = ct * 512 + cg * 8, wide = s.wide();
     const int64_t plane = s.M * wide;
     constexpr bool KEPT = ACT != kActNone || GATED;
@@ -667,7 +686,7 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
             st16(dz + n * plane + at, out);
         }
     };
-    for (int64_t r0 = run * kDzRows + sub; r0 < end; r0 += rows * AT_ONCE) {
+    for (int64_t r0 = run * run_rows + sub; r0 < end; r0 += rows * AT_ONCE) {
         vec16 gv[AT_ONCE][D] = {}, zv[AT_ONCE] = {}, uv[AT_ONCE] = {};
 #pragma unroll
         for (int i = 0; i < AT_ONCE; ++i) {
@@ -719,12 +738,12 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
     }
 }
 
-// The runs' sums: 16 threads to a column, each with a 16th of the runs, added in
-// order; with no runs, 0.
-__global__ __launch_bounds__(256) void ep_linear_bias_kernel(const float *__restrict__ sums, int64_t runs, int wide,
-                                                             float *__restrict__ out) {
+// The runs' sums: 16 columns a block and 16 threads to a column, each with a 16th
+// of the runs, added in order; with no runs, 0.
+__device__ __forceinline__ void add_runs(const float *__restrict__ sums, int64_t runs, int wide, float *__restrict__ out,
+                                         uint32_t block) {
     __shared__ float part[16][16];
-    const int lane = threadIdx.x % 16, group = threadIdx.x / 16, c = blockIdx.x * 16 + lane;
+    const int lane = threadIdx.x % 16, group = threadIdx.x / 16, c = block * 16 + lane;
     float v = 0.0f;
     if (c < wide)
         for (int64_t i = runs * group / 16; i < runs * (group + 1) / 16; ++i) v += sums[i * wide + c];
@@ -735,6 +754,32 @@ __global__ __launch_bounds__(256) void ep_linear_bias_kernel(const float *__rest
 #pragma unroll
     for (int i = 0; i < 16; ++i) v += part[i][lane];
     out[c] = v;
+}
+__global__ __launch_bounds__(256) void ep_linear_bias_kernel(const float *__restrict__ sums, int64_t runs, int wide,
+                                                             float *__restrict__ out) {
+    add_runs(sums, runs, wide, out, blockIdx.x);
+}
+
+// The three gradients of a small call in one launch: blocks of the one over x,
+// then those over w, then the bias'.
+struct Gradients {
+    Product x, w;
+    uint32_t xblocks, wblocks;
+    const float *sums;
+    int64_t runs;
+    int wide;
+    float *bias;
+};
+typedef Tile<false, true, false, 64, 64, 4, 1, 64, 4, 1> SmallX;
+typedef Tile<true, true, false, 64, 64, 4, 1, 64, 4, 1> SmallW;
+__global__ __launch_bounds__(256) void ep_linear_gradients_kernel(Gradients g) {
+    static_assert(SmallX::THREADS == 256 && SmallW::THREADS == 256, "one kind of block");
+    if (blockIdx.x < g.xblocks)
+        SmallX::run(g.x, blockIdx.x);
+    else if (blockIdx.x - g.xblocks < g.wblocks)
+        SmallW::run(g.w, blockIdx.x - g.xblocks);
+    else
+        add_runs(g.sums, g.runs, g.wide, g.bias, blockIdx.x - g.xblocks - g.wblocks);
 }
 
 __global__ __launch_bounds__(256) void ep_linear_zero_kernel(vec16 *out, int64_t n) {
@@ -760,9 +805,13 @@ hipError_t launch_linear(const LinearShape &s, const uint16_t *x, const uint16_t
     p.act = s.act;
     p.gated = s.gated;
     p.linear = true;
+    // Few rows: the weights' bytes are the time, and the tile form has too few blocks
+    // to fetch them.  Stream / tile form, us: 16 rows 7168 -> 2048 x 2 15 / 26; 32 rows
+    // 7168 -> 7168 20.5 / 25, 7168 -> 2048 x 2 20.7 / 22.8, 4096 -> 4096 12.9 / 15.7;
+    // from 128 tiles of 64 columns on it has enough (4096 -> 8192 16.4 / 15.9,
+    // -> 16384 28 / 23).
     if (s.M <= 16) return s.gated ? launch_stream<true, 1>(p, stream) : launch_stream<false, 1>(p, stream);
-    if (s.M <= 32) return s.gated ? launch_stream<true, 2>(p, stream) : launch_stream<false, 2>(p, stream);
-    if (s.M <= 64) return s.gated ? launch_stream<true, 4>(p, stream) : launch_stream<false, 4>(p, stream);
+    if (s.M <= 32 && s.wide() < 128 * 64) return s.gated ? launch_stream<true, 2>(p, stream) : launch_stream<false, 2>(p, stream);
     return s.gated ? launch_product<false, false, true>(p, stream) : launch_product<false, false, false>(p, stream);
 }
 
@@ -785,7 +834,8 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
     const int parts = s.plain() ? 0 : (s.w32 && grad_w ? 3 : 1);
     uint16_t *dz = reinterpret_cast<uint16_t *>(ws);
     float *sums = reinterpret_cast<float *>(ws + linear_sums_offset(s));
-    const int64_t runs = (s.M + kDzRows - 1) / kDzRows;
+    const int run_rows = dz_rows(s);
+    const int64_t runs = (s.M + run_rows - 1) / run_rows;
     if (grad_bias || (parts > 0 && (grad_x || grad_w))) {
         const dim3 grid((unsigned)(runs * ((s.N + 511) / 512)));
         int shift = 0;   // threads to a row
@@ -795,7 +845,7 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
             with_activation(s.act, [&](auto act) {
                 hipLaunchKernelGGL((ep_linear_dz_kernel<Dy, decltype(act)::value, decltype(gated)::value != 0>), grid,
                                    dim3(kDzThreads), 0, stream, s, from, z, dz, parts, grad_bias ? sums : nullptr,
-                                   shift);
+                                   shift, run_rows);
             });
         };
         if (s.f32)
@@ -804,35 +854,46 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
             s.gated ? launch(static_cast<const uint16_t *>(dy), Const<1>())
                     : launch(static_cast<const uint16_t *>(dy), Const<0>());
     }
-    if (grad_bias)
-        hipLaunchKernelGGL(ep_linear_bias_kernel, dim3((unsigned)((wide + 15) / 16)), dim3(256), 0, stream, sums,
-                           runs, wide, grad_bias);
-    hipError_t e = grad_x || grad_w || grad_bias ? hipGetLastError() : hipSuccess;
-    if (e != hipSuccess) return e;
     const uint16_t *d = parts > 0 ? dz : static_cast<const uint16_t *>(dy);
-    if (grad_x) {
-        Product p = {};
-        p.r = {d, s.M, wide, 0};
-        p.q = {w, s.K, s.K, 0};
-        p.k = wide;
-        p.parts = 1;
-        p.out_ld = s.K;
-        p.out = grad_x;
-        e = launch_product<false, true, false>(p, stream);
-        if (e != hipSuccess) return e;
+    Gradients g = {};
+    g.sums = sums;
+    g.runs = runs;
+    g.wide = wide;
+    g.bias = grad_bias;
+    g.x.r = {d, s.M, wide, 0};
+    g.x.q = {w, s.K, s.K, 0};
+    g.x.k = wide;
+    g.x.parts = 1;
+    g.x.out_ld = s.K;
+    g.x.out = grad_x;
+    g.w.r = {d, wide, wide, 0};
+    g.w.q = {x, s.K, s.K, 0};
+    g.w.k = s.M;
+    g.w.parts = parts > 1 ? parts : 1;
+    g.w.part = s.M * wide;
+    g.w.out_ld = s.K;
+    g.w.out = grad_w;
+    g.w.out_f32 = s.w32;
+    const unsigned columns = grad_bias ? (unsigned)((wide + 15) / 16) : 0;
+    // Small calls: what counts is the launches.  The sums are short enough for one
+    // wave of blocks, and those of both products have room on the chip at once.
+    if (grad_x && grad_w && tile_count(g.x, 64, 64) + tile_count(g.w, 64, 64) <= 512 && wide <= 1024 &&
+        s.M * g.w.parts <= 1024) {
+        const auto tiles = [](Product &p) {
+            p.rtiles = (int)((p.r.rows + 63) / 64);
+            p.ctiles = (int)((p.out_ld + 63) / 64);
+            return (uint32_t)Order{p.rtiles, p.ctiles}.blocks();
+        };
+        g.xblocks = tiles(g.x);
+        g.wblocks = tiles(g.w);
+        hipLaunchKernelGGL(ep_linear_gradients_kernel, dim3(g.xblocks + g.wblocks + columns), dim3(256), 0, stream, g);
+        return hipGetLastError();
     }
-    if (grad_w) {
-        Product p = {};
-        p.r = {d, wide, wide, 0};
-        p.q = {x, s.K, s.K, 0};
-        p.k = s.M;
-        p.parts = parts > 1 ? parts : 1;
-        p.part = s.M * wide;
-        p.out_ld = s.K;
-        p.out = grad_w;
-        p.out_f32 = s.w32;
-        e = launch_product<true, true, false>(p, stream);
-    }
+    if (grad_bias)
+        hipLaunchKernelGGL(ep_linear_bias_kernel, dim3(columns), dim3(256), 0, stream, sums, runs, wide, grad_bias);
+    hipError_t e = grad_x || grad_w || grad_bias ? hipGetLastError() : hipSuccess;
+    if (grad_x && e == hipSuccess) e = launch_product<false, true, false>(g.x, stream);
+    if (grad_w && e == hipSuccess) e = launch_product<true, true, false>(g.w, stream);
     return e;
 }
 

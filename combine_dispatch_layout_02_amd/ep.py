@@ -803,6 +803,10 @@ def ep_linear_backward(dy, x, w, z, grad_x, grad_w, grad_bias, ws, activation=No
     """Gradients of ep_linear from dy and the z it kept (None where there is
     neither activation nor gate); those that are None are not computed."""
     sh = _linear_shape(x, w, activation, gated, dy.dtype, torch.bfloat16 if grad_w is None else grad_w.dtype)
+    _linear_backward(sh, dy, x, w, z, grad_x, grad_w, grad_bias, ws, activation, gated, stream)
+
+
+def _linear_backward(sh, dy, x, w, z, grad_x, grad_w, grad_bias, ws, activation, gated, stream):
     M, N, wide = x.shape[0], sh.out_features, w.shape[0]
     _need(dy, dy.dtype, (M, N), "dy")
     if activation is not None or gated:
@@ -1100,5 +1104,5 @@ def linear_backward(dy, x, w, z=None, activation=None, gated=False, bias=False, 
         ws, = _alloc(x, (n.value, torch.uint8), stream=stream)
     gx, gw = _alloc(x, (x.shape, torch.bfloat16), (w.shape, grad_w_dtype), stream=stream)
     gb = _alloc(x, (w.shape[0], torch.float32), stream=stream)[0] if bias else None
-    ep_linear_backward(dy, x, w, z, gx, gw, gb, ws, activation, gated, stream)
+    _linear_backward(sh, dy, x, w, z, gx, gw, gb, ws, activation, gated, stream)
     return (gx, gw, gb) if bias else (gx, gw)

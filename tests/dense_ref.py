@@ -126,8 +126,8 @@ def linear_backward(dy, x, w, z, act, gated, parts):
     ex = ex @ w.abs() + sum_error(mx, w.shape[0])
     ew = ew.T @ x.abs() + sum_error(mw, max(parts, 1) * x.shape[0])
     gb, mb = dz.sum(0), dz.abs().sum(0)
-    # runs of 32 rows, added in some order, then 16 parts of the runs
-    eb = e.sum(0) + STEP * (32 + len(dz) / 512 + 1 + 16) * (mb + e.sum(0))
+    # runs of 4 to 64 rows, added in some order, then 16 parts of the runs
+    eb = e.sum(0) + STEP * (64 + len(dz) / 64 + 1 + 16) * (mb + e.sum(0))
     return (gx, ex), (gw, ew), (gb, eb)
 
 
