@@ -489,18 +489,14 @@ hipError_t launch_product(const Product &p, hipStream_t stream) {
 
 // One block: 16 G weight rows (gated: 8 G of each half) by up to 16 MT rows of
 // x, NW waves with a part of K each; the weights' bytes are the time.
-template <bool GATED, int G, int MT, int NW, int NB>
+template <bool GATED, int G, int MT, int NW>
 __global__ __launch_bounds__(64 * NW) void ep_linear_stream_kernel(Product p, int ctiles) {
     typedef Step<false, G> S;
     constexpr int KE = S::KE, C = S::CHUNKS;
     __shared__ __attribute__((aligned(16))) uint8_t buf0[NW * G * 2048];
     __shared__ __attribute__((aligned(16))) uint8_t buf1[NW * G * 2048];
-    __shared__ __attribute__((aligned(16))) uint8_t buf2[NB > 2 ? NW * G * 2048 : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t buf3[NB > 3 ? NW * G * 2048 : 16];
-    static_assert(NB == 2 || NB == 4, "as many buffers");
-    const auto buf = [&](int j) {
-        return j % NB == 0 ? buf0 : (j % NB == 1 ? buf1 : (j % NB == 2 ? buf2 : buf3));
-    };
+    constexpr int NB = 2;
+    const auto buf = [&](int j) { return j % NB ? buf1 : buf0; };
     const int c0 = (int)(blockIdx.x % ctiles) * (GATED ? 8 * G : 16 * G);
     const int64_t r0 = (int64_t)(blockIdx.x / ctiles) * 16 * MT;
     const int rows = (int)min(p.r.rows - r0, (int64_t)16 * MT);
@@ -618,24 +614,26 @@ __global__ __launch_bounds__(64 * NW) void ep_linear_stream_kernel(Product p, in
     }
 }
 
-template <bool GATED, int G, int MT, int NW, int NB>
+template <bool GATED, int G, int MT, int NW>
 hipError_t launch_stream(const Product &p, hipStream_t stream) {
     const int wide = GATED ? 8 * G : 16 * G, ctiles = (int)((p.out_ld + wide - 1) / wide);
     const int64_t blocks = ctiles * ((p.r.rows + 16 * MT - 1) / (16 * MT));
-    hipLaunchKernelGGL((ep_linear_stream_kernel<GATED, G, MT, NW, NB>), dim3((unsigned)blocks), dim3(64 * NW), 0, stream,
+    hipLaunchKernelGGL((ep_linear_stream_kernel<GATED, G, MT, NW>), dim3((unsigned)blocks), dim3(64 * NW), 0, stream,
                        p, ctiles);
     return hipGetLastError();
 }
 
-// 16 weight rows a block while every one has a CU of its own, else 32 and half the
-// waves (x 1 or 16 rows; 16 / 32 weight rows a block, us):
-//   7168 -> 1024  11.6 / 12.4     2048 -> 7168     11.8 / 6.7
-//   4096 -> 4096   9.0 / 9.1      7168 -> 7168     26.3 / 17.8
-//   7168 -> 2048 x 2, 1 row  12.9 / 11.9           4096 -> 16384  34.3 / 25.3
+// 16 weight rows a block and 8 waves while every block has a CU of its own, else 32
+// and 4 (us for 16 rows of x; 16 x 8 / 32 x 4):
+//   7168 -> 1024 10.7 / 11.9    2048 -> 7168       8.2 / 6.3
+//   4096 -> 4096  8.0 / 9.2     7168 -> 7168      21.0 / 17.5
+//   7168 -> 2048 x 2 12.5 / 14.8    4096 -> 16384 23.9 / 22.4
+// Twice the waves or four steps ahead instead of two take a CU's LDS for one block,
+// and the next one has to wait for it to end: 15.2 for the 12.5.
 template <bool GATED, int MT>
 hipError_t launch_stream(const Product &p, hipStream_t stream) {
-    if ((GATED ? 2 : 1) * p.out_ld > 16 * 256) return launch_stream<GATED, 2, MT, 8, 2>(p, stream);
-    return launch_stream<GATED, 1, MT, 16, 4>(p, stream);
+    if ((GATED ? 2 : 1) * p.out_ld > 16 * 256) return launch_stream<GATED, 2, MT, 4>(p, stream);
+    return launch_stream<GATED, 1, MT, 8>(p, stream);
 }
 
 // ---------------------------------------------------------------- the gradient over z
