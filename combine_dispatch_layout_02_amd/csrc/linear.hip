@@ -873,10 +873,12 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
     g.w.out = grad_w;
     g.w.out_f32 = s.w32;
     const unsigned columns = grad_bias ? (unsigned)((wide + 15) / 16) : 0;
-    // Small calls: what counts is the launches.  The sums are short enough for one
-    // wave of blocks, and those of both products have room on the chip at once.
-    if (grad_x && grad_w && tile_count(g.x, 64, 64) + tile_count(g.w, 64, 64) <= 512 && wide <= 1024 &&
-        s.M * g.w.parts <= 1024) {
+    // Small calls: what counts is the launches (100 rows 512 -> 512: 28.1 us for all
+    // with three of them, 20.5 with one).  Both products' blocks have room on the
+    // chip at once (two a CU), and sums below 1024 are those that launch_product does
+    // not halve: a gradient that is asked for alone has the same bits.
+    if (grad_x && grad_w && tile_count(g.x, 64, 64) + tile_count(g.w, 64, 64) <= 512 && wide < 1024 &&
+        s.M * g.w.parts < 1024) {
         const auto tiles = [](Product &p) {
             p.rtiles = (int)((p.r.rows + 63) / 64);
             p.ctiles = (int)((p.out_ld + 63) / 64);

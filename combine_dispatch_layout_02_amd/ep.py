@@ -757,9 +757,13 @@ def ep_moe_few(x, topk_idx, topk_w, gate_up, gate_up_scales, down, down_scales, 
     _ok(load().ep_moe_few(ctypes.byref(sh), *args, ws.numel(), raw), "ep_moe_few")
 
 
-def _linear_shape(x, w, activation, gated, y_dtype, grad_w_dtype=torch.bfloat16) -> ep_linear_shape:
+def _known(activation):
     if activation not in _ACTIVATIONS:
         raise ValueError(f"activation: expected one of {list(_ACTIVATIONS)}, got {activation!r}")
+
+
+def _linear_shape(x, w, activation, gated, y_dtype, grad_w_dtype=torch.bfloat16) -> ep_linear_shape:
+    _known(activation)
     for dtype, name in ((y_dtype, "y"), (grad_w_dtype, "grad_w")):
         if dtype not in (torch.float32, torch.bfloat16):
             raise ValueError(f"{name}: expected float32 or bfloat16, got {dtype}")
@@ -791,6 +795,7 @@ def ep_linear(x, w, bias, residual, y, z=None, activation=None, gated=False, str
 def linear_backward_workspace_bytes(M, K, N, activation=None, gated=False, y_dtype=torch.bfloat16,
                                     grad_w_dtype=torch.bfloat16) -> int:
     """Bytes of the workspace ep_linear_backward takes."""
+    _known(activation)
     sh = ep_linear_shape(int(M), int(K), int(N), _ACTIVATIONS[activation], int(bool(gated)),
                          int(y_dtype == torch.float32), int(grad_w_dtype == torch.float32))
     n = ctypes.c_size_t()

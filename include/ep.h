@@ -643,7 +643,8 @@ int ep_moe_few_workspace_bytes(const ep_few_shape *shape, size_t *bytes);
  *   residual  [T, H] bf16 or NULL
  *   y         [T, H] bf16; it may be x's or residual's buffer and overlaps no other input
  *   ws        ep_moe_few_workspace_bytes, 256-byte aligned; it needs no clearing
- *             and holds nothing from one call to the next
+ *             and holds nothing from one call to the next.  Calls that share one
+ *             must not overlap in time (one stream, or ordered by events).
  * x, gate_up, down, residual and y are 16-byte aligned.
  */
 int ep_moe_few(const ep_few_shape *shape, const uint16_t *x, const int64_t *topk_idx, const float *topk_w,
@@ -698,17 +699,18 @@ int ep_linear_backward_workspace_bytes(const ep_linear_shape *shape, size_t *byt
  * Gradients of ep_linear from the gradient dy of its result and the z it kept:
  *     dz = dy * act'(z)     gated: [dy * z[:, N:] * act'(z[:, :N]), dy * act(z[:, :N])]
  *     grad_x = dz w, grad_w = dz^T x, grad_bias = sum over rows of dz
- * (that of the residual is dy itself; relu' is 0 at 0).  dz is computed in fp32.  For the two
- * products it is rounded to bf16, half a step of which is what the rounding of
- * their bf16 results is; for an fp32 grad_w it enters as three bf16 parts, which
- * lose nothing, unless it is dy itself.  grad_bias is the sum of the fp32 values, in fp32, in a fixed
- * order.  Deterministic for a shape.
+ * (that of the residual is dy itself; relu' is 0 at 0).  dz is computed in fp32.
+ * For the two products it is rounded to bf16, half a step of which is what the
+ * rounding of their bf16 results is; for an fp32 grad_w it enters as three bf16
+ * parts, which lose nothing, unless it is dy itself.  grad_bias is the sum of the
+ * fp32 values, in fp32, in a fixed order.  Deterministic for a shape.
  *   dy [M, N] bf16 or fp32 (y_f32); z [M, N or 2 N] bf16, NULL where there is
  *   neither activation nor gate; x, w as for ep_linear
  *   grad_x [M, K] bf16, grad_w [N or 2 N, K] bf16 or fp32 (grad_w_f32),
  *   grad_bias [N or 2 N] fp32: each may be NULL, and is then not computed; they overlap no input
  *   With no rows, grad_w and grad_bias are 0.
- *   ws 256-byte aligned; it needs no clearing and holds nothing from one call to the next
+ *   ws 256-byte aligned; it needs no clearing and holds nothing from one call to the next;
+ *   calls that share one must not overlap in time (one stream, or ordered by events)
  * dy, z, x, w, grad_x and grad_w are 16-byte aligned.
  */
 int ep_linear_backward(const ep_linear_shape *shape, const void *dy, const uint16_t *x, const uint16_t *w,

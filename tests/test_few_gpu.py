@@ -1,7 +1,6 @@
 """ep_moe_few against its 64-bit implementation: both weight formats, one token
 to the limit, masked slots and tokens, experts named twice, all tokens on one
-expert, odd sizes; in place, captured, on two streams at once; beside the chain
-of the framework's other calls."""
+expert, odd sizes, values at the ends of the types; in place."""
 import pytest
 
 import dense_ref as ref

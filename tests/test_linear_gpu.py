@@ -218,3 +218,17 @@ def test_large_tiles(ep, M, K, N, act, gated):
         want = ref.linear_backward(dy, c["x"], c["w"], zz, act, gated, 0 if plain else (3 if w32 else 1))
         for g, (v, e), half in zip(got, want, (ref.BF16_HALF, ref.F32_HALF if w32 else ref.BF16_HALF, ref.F32_HALF)):
             ref.check(g, v, e, half)
+
+
+@pytest.mark.parametrize("M", [1, 7, 16, 17, 24, 32, 33])
+@pytest.mark.parametrize("K", [8, 72, 1000, 2048])
+@pytest.mark.parametrize("N,act,gated,f32", [(4096, None, False, False), (4104, "gelu", False, True),
+                                             (2056, "silu", True, False), (2504, None, True, True),
+                                             (8184, None, False, False), (8200, "relu", False, True)])
+def test_few_rows_of_wide_layers(ep, M, K, N, act, gated, f32):
+    """At the widths and rows where the forms change."""
+    d = _draw(M, K, N, gated, True, True, seed=2)
+    y, z = ep.linear(*_cuda(d).values(), activation=act, gated=gated, out_dtype=F32 if f32 else BF, save=True)
+    wy, ey, wz, ez = ref.linear(*d.values(), act, gated)
+    ref.check(z.cpu(), wz, ez, ref.BF16_HALF)
+    ref.check(y.cpu(), wy, ey, ref.F32_HALF if f32 else ref.BF16_HALF)
