@@ -282,21 +282,24 @@ struct Order {
 // s + 1 are read and the operands of s + NB are on their way into the place of s,
 // which every wave had read before the barrier.  Where tiles are few, SK such
 // groups of waves each take a part of the steps, and the first adds up the sums
-// in order.
-template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK>
+// in order.  With P parts of R beside each other, every step has those of all, each
+// with sums of its own, and Q is brought once for them; with P 1 they follow each
+// other (p.parts).
+template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK, int P>
 struct Tile {
-    static constexpr int W = WR * WC, THREADS = 64 * W * SK, NR = BR / WR / 16, NC = BC / WC / 16, CH = KS / 32;
+    static constexpr int W = WR * WC, THREADS = 64 * W * SK, ROWS = BR / WR / 16, NR = P * ROWS, NC = BC / WC / 16,
+                         CH = KS / 32;
     static_assert(NC % (GATED ? 4 : 2) == 0, "pairs of groups of columns, of a gate's and of their factors, in one wave");
     static_assert(NB >= 2 && NB <= 4, "as many buffers");
     typedef Side<TR, BR, W, KS> R;
     typedef Side<TQ, BC, W, KS> Q;
-    static constexpr int BYTES = R::BYTES + Q::BYTES;
+    static constexpr int RBYTES = P * R::BYTES, BYTES = RBYTES + Q::BYTES;
     static_assert(SK == 1 || (W * NC * NR * 1024 <= SK * BYTES && SK <= NB + 1), "a buffer takes the sums of a part");
     static __device__ __forceinline__ void run(const Product &p, uint32_t block);
 };
 
-template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK>
-__device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK>::run(const Product &p, uint32_t block) {
+template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK, int P>
+__device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK, P>::run(const Product &p, uint32_t block) {
     __shared__ __attribute__((aligned(16))) uint8_t buf0[SK * BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t buf1[SK * BYTES];
     __shared__ __attribute__((aligned(16))) uint8_t buf2[NB > 2 ? SK * BYTES : 16];
@@ -319,7 +322,7 @@ __device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK>:
     Q lq;
     lr.init(p.r, r0, wr * (BR / WR), lane, wid);
     lq.init(p.q, c0, cw, lane, wid);
-    constexpr int L = R::NL + Q::NL;
+    constexpr int LR = P * R::NL, L = LR + Q::NL;
     const int k = (int)p.k, steps = (k + KS - 1) / KS, all = steps * p.parts;
     // this group's steps: as many for each (barriers), the last one's may lie past the sum
     const int share = (all + SK - 1) / SK, s0 = sk * share;
@@ -340,10 +343,10 @@ __device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK>:
         if (--todo <= 0) left = 0;
     };
     const auto stage = [&](uint8_t *to, int i) {   // load i of the wave
-        if (i < R::NL)
-            lr.load(to, i, wid, rp, left);
+        if (i < LR)
+            lr.load(to + i / R::NL * R::BYTES, i % R::NL, wid, rp + i / R::NL * p.part, left);
         else
-            lq.load(to + R::BYTES, i - R::NL, wid, qp, left);
+            lq.load(to + RBYTES, i - LR, wid, qp, left);
         if (i == L - 1) advance();
     };
     struct Fragments {   // of 32 of k
@@ -351,9 +354,9 @@ __device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK>:
     };
     const auto read = [&](const uint8_t *from, Fragments &f, int c, int i) {   // fragment i of part c of a step
         if (i < NC)
-            f.q[i] = lq.fragment(from + R::BYTES, qrow(i), c);
+            f.q[i] = lq.fragment(from + RBYTES, qrow(i), c);
         else
-            f.r[i - NC] = lr.fragment(from, 16 * (i - NC), c);
+            f.r[i - NC] = lr.fragment(from + (i - NC) / ROWS * R::BYTES, 16 * ((i - NC) % ROWS), c);
     };
 
     f32x4 acc[NC][NR] = {};
@@ -420,23 +423,34 @@ __device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK>:
             for (int i = 0; i < NC * NR; ++i) acc[i / NR][i % NR] += sums(q)[i * kWave];
     }
 
+    if constexpr (P > 1)   // the smallest parts first
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+#pragma unroll
+            for (int m = 0; m < ROWS; ++m) {
+                f32x4 v = acc[i][(P - 1) * ROWS + m];
+#pragma unroll
+                for (int q = P - 2; q >= 0; --q) v += acc[i][q * ROWS + m];
+                acc[i][m] = v;
+            }
+
     // pairs of groups of columns; the residual's values are all on their way before the first is used
     const int r16 = lane & 15, quad = lane >> 4;
     constexpr int PAIRS = GATED ? NC / 4 : NC / 2, HALF = GATED ? NC / 2 : 0;   // without a gate the factors are not looked at
     const auto row = [&](int m) { return r0 + wr * (BR / WR) + 16 * m + r16; };
     const auto column = [&](int f) { return c0 + cw + 32 * f + Eight::column(quad); };
     const auto inside = [&](int f, int m) { return row(m) < p.r.rows && column(f) < p.out_ld; };
-    vec16 residual[PAIRS][NR] = {};
+    vec16 residual[PAIRS][ROWS] = {};
     if (p.residual)
 #pragma unroll
         for (int f = 0; f < PAIRS; ++f)
 #pragma unroll
-            for (int m = 0; m < NR; ++m)
+            for (int m = 0; m < ROWS; ++m)
                 if (inside(f, m)) residual[f][m] = ld16(p.residual + row(m) * p.out_ld + column(f));
 #pragma unroll
     for (int f = 0; f < PAIRS; ++f) {
 #pragma unroll
-        for (int m = 0; m < NR; ++m) {
+        for (int m = 0; m < ROWS; ++m) {
             const Eight v(acc[2 * f][m], acc[2 * f + 1][m]), u(acc[2 * f + HALF][m], acc[2 * f + 1 + HALF][m]);
             if (inside(f, m)) finish(p, row(m), column(f), v, u, residual[f][m]);
         }
@@ -448,9 +462,10 @@ __global__ __launch_bounds__(T::THREADS) void ep_linear_tile_kernel(Product p) {
     T::run(p, blockIdx.x);
 }
 
-template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK = 1>
+template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK = 1, int P = 1>
 hipError_t launch_tile(Product p, hipStream_t stream) {
-    typedef Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK> T;
+    typedef Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK, P> T;
+    if (P > 1) p.parts = 1;
     const int cols = GATED ? BC / 2 : BC;
     p.rtiles = (int)((p.r.rows + BR - 1) / BR);
     p.ctiles = (int)((p.out_ld + cols - 1) / cols);
@@ -465,21 +480,42 @@ int64_t tile_count(const Product &p, int BR, int BC) {
 }
 
 // The largest tile that still gives 160 blocks (of 256 CUs), as a larger one reads
-// less of LDS and memory for a product: with us at both sides
-//   4096 rows 7168 -> 2048 x 2   256 x 256 tiles 189, 128 x 128 276
-//   4096 rows 2048 -> 7168       256 x 256       133, 128 x 128 137
+// less of LDS and memory for a product, by 8 waves as far as pairs of groups of
+// columns go; in us:
+//   4096 rows 7168 -> 2048 x 2   256 x 256 tiles 195, 128 x 128 236, 256 x 128 242
+//   2048 rows 2048 -> 7168       256 x 256 tiles 73, 128 x 128 80
 //   1024 rows 7168 -> 2048       64 x 128 (256 tiles) 37.5, 128 x 128 (128) 62, 64 x 64 (512) 46
 //   512 rows 4096 -> 4096        64 x 128 (256) 24.0, 128 x 128 (128) 37.6, 64 x 64 (512) 27.5
-// and where even those of 64 x 64 are 128 at most, two groups of waves with half
-// the steps each, if those are 16 or more:
+// The weights' gradient, whose operands both come by lines of k, gains by 256 x 128
+// in between (4096 x 2048 from 4096 rows 62, 128 x 128 72; 2560 x 2048 from 16384
+// rows 171 / 221), the other products lose (2048 rows 4096 -> 4096 77 / 73).
+// 128 x 128 tiles by 8 waves at 64 of k a step against 4 at 32 (two blocks a CU):
+// 1024 rows 7168 -> 2048 x 2 59 / 75, 2048 rows 4096 -> 2048 36 / 41; 64 x 128 ones
+// by 8 waves against 4: 512 rows 4096 -> 4096 24.5 / 26.8, but with a gate, where
+// a wave has a gate's columns and their factors', 45.3 / 44.0.
+// Where even those of 64 x 64 are 128 at most, two groups of waves with half the
+// steps each, if those are 16 or more:
 //   64 rows 7168 -> 2048 x 2 27.9, halved 24.3;  100 rows 4096 -> 4096 18.1, 16.1
 //   300 rows 4096 -> 1024    17.8, halved 15.5;  512 rows 7168 -> 256  28.6, 24.9
 template <bool TR, bool TQ, bool GATED>
 hipError_t launch_product(const Product &p, hipStream_t stream) {
     const auto tiles = [&](int BR, int BC) { return tile_count(p, BR, BC); };
+    // Three parts of dz beside each other where tiles of 64 x 128 are 64 or more, and
+    // those of 256 x 256 too few (weights' gradients with dz's kernel, us, beside /
+    // after each other: 256 x 7168 from 4096 rows 53 / 83, 512 x 7168 82 / 114; 128 x
+    // 2048 from 1024 rows, 32 tiles, 18.4 / 16.8; 4096 x 7168 from 1024 rows, in
+    // tiles of 256 x 256 where their sums find no registers, 181 / 164).  Not for
+    // short sums, which may come in one launch with the other gradients.
+    if constexpr (TR)
+        if (p.parts == 3 && 3 * p.k >= 1024 && tiles(256, 256) < 160) {
+            if (tiles(128, 128) >= 160) return launch_tile<TR, TQ, GATED, 128, 128, 4, 2, 32, 4, 1, 3>(p, stream);
+            if (tiles(64, 128) >= 64) return launch_tile<TR, TQ, GATED, 64, 128, 2, 4, 64, 3, 1, 3>(p, stream);
+        }
     if (tiles(256, 256) >= 160) return launch_tile<TR, TQ, GATED, 256, 256, 2, 4, 32, 4>(p, stream);
-    if (tiles(128, 128) >= 160) return launch_tile<TR, TQ, GATED, 128, 128, 2, 2, 32, 4>(p, stream);
-    if (tiles(64, 128) >= 160) return launch_tile<TR, TQ, GATED, 64, 128, 2, 2, 64, 4>(p, stream);
+    if constexpr (TR)
+        if (tiles(256, 128) >= 160) return launch_tile<TR, TQ, GATED, 256, 128, 4, 2, 32, 4>(p, stream);
+    if (tiles(128, 128) >= 160) return launch_tile<TR, TQ, GATED, 128, 128, GATED ? 4 : 2, GATED ? 2 : 4, 64, 4>(p, stream);
+    if (tiles(64, 128) >= 160) return launch_tile<TR, TQ, GATED, 64, 128, 2, GATED ? 2 : 4, 64, 4>(p, stream);
     if (tiles(64, 64) <= 128 && p.k * p.parts >= 1024)
         return launch_tile<TR, TQ, GATED, 64, 64, 4, 1, 64, 4, 2>(p, stream);
     return launch_tile<TR, TQ, GATED, 64, 64, 4, 1, 64, 4>(p, stream);
@@ -768,8 +804,8 @@ struct Gradients {
     int wide;
     float *bias;
 };
-typedef Tile<false, true, false, 64, 64, 4, 1, 64, 4, 1> SmallX;
-typedef Tile<true, true, false, 64, 64, 4, 1, 64, 4, 1> SmallW;
+typedef Tile<false, true, false, 64, 64, 4, 1, 64, 4, 1, 1> SmallX;
+typedef Tile<true, true, false, 64, 64, 4, 1, 64, 4, 1, 1> SmallW;
 __global__ __launch_bounds__(256) void ep_linear_gradients_kernel(Gradients g) {
     static_assert(SmallX::THREADS == 256 && SmallW::THREADS == 256, "one kind of block");
     if (blockIdx.x < g.xblocks)

@@ -200,7 +200,8 @@ def test_refusals(ep):
 @pytest.mark.parametrize("M,K,N,act,gated", [(4100, 200, 2600, "silu", True), (5000, 96, 2056, "gelu", False),
                                              (1600, 1608, 1800, None, False), (2050, 520, 1040, "silu", True),
                                              (700, 4104, 5000, "relu", False), (4096, 136, 7168, "silu", False),
-                                             (3500, 7168, 520, None, False)], ids=str)
+                                             (3500, 7168, 520, None, False), (905, 2600, 2312, "gelu_tanh", False),
+                                             (1031, 1032, 1288, None, True)], ids=str)
 def test_large_tiles(ep, M, K, N, act, gated):
     """Enough rows and columns for the wider tiles of each product, with ragged ends."""
     d = _draw(M, K, N, gated, True, not gated, seed=4)
