@@ -543,7 +543,7 @@ __global__ __launch_bounds__(64 * NW) void ep_few_down_kernel(
             const uint2 r = *reinterpret_cast<const uint2 *>(residual + o);
             v += f32x4{bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y)};
         }
-        *reinterpret_cast<uint2 *>(y + o) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        *reinterpret_cast<uint2 *>(y + o) = uint2{pack_bf16x2_cvt(v[0], v[1]), pack_bf16x2_cvt(v[2], v[3])};
     };
     if (parts == 1) {
         each([&](int t, int at, size_t o) { finish(sum_up(t, at), o); });

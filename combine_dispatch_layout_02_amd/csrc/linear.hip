@@ -225,8 +225,8 @@ struct Eight {
         *reinterpret_cast<f32x4 *>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
     }
     __device__ __forceinline__ void store(uint16_t *p) const {
-        st16(p, vec16{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                      pack_bf16x2(v[6], v[7])});
+        st16(p, vec16{pack_bf16x2_cvt(v[0], v[1]), pack_bf16x2_cvt(v[2], v[3]), pack_bf16x2_cvt(v[4], v[5]),
+                      pack_bf16x2_cvt(v[6], v[7])});
     }
     __device__ __forceinline__ void store(void *out, bool f32, int64_t at) const {
         if (f32)
@@ -702,6 +702,11 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
         for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(v[i]), f[2 * i + 1] = bf16_hi(v[i]);
     };
     const auto store = [&](int64_t at, float (&f)[8]) {
+        if (parts == 1) {
+            st16(dz + at, vec16{pack_bf16x2_cvt(f[0], f[1]), pack_bf16x2_cvt(f[2], f[3]), pack_bf16x2_cvt(f[4], f[5]),
+                                pack_bf16x2_cvt(f[6], f[7])});
+            return;
+        }
         for (int n = 0; n < parts; ++n) {
             vec16 out;
 #pragma unroll
