@@ -6,11 +6,16 @@
 //
 // At this size each expert's weights serve a few rows, and their bytes are the
 // time: 3 H I of them for every expert that a token has, read once.  Both
-// kernels stream them through LDS by direct loads, 4 KiB (32 rows by 128
-// bytes) a wave and step, two steps ahead, without a barrier; the products run
+// kernels stream them through LDS by direct loads, 64 or 32 rows by 128 bytes a
+// wave and step, two or four steps ahead, without a barrier; the products run
 // in 16-bit matrix instructions, with e4m3 weights widened to bf16 (exactly)
 // on their way.  The weights are the first operand, the tokens' rows the
 // second, so a lane's 4 results lie at consecutive columns of one token.
+//
+// Measured, first + second kernel: one token, 8 experts of 7168 x 2048 in e4m3,
+// 45 + 29 us (5.2 and 4.1 TB/s); 32 tokens over 64 such experts, top-8, 306 + 165
+// (6.1 and 5.7; a large plain read reaches 6.8); 64 tokens, 96 experts of 2048 x
+// 1408, top-6, 117 + 64 (4.7 and 4.3: K or I in waves' parts of few steps).
 //
 // No expert's rows are gathered first: a block of the first kernel finds its
 // expert and that one's tokens in topk_idx by itself, and one extra block writes
