@@ -12,12 +12,12 @@
 // transposing LDS read.  Q is the instruction's first operand, R its second, so
 // a lane's 4 results lie at consecutive c.
 //
-// Measured: 4096 rows 7168 -> 2 x 2048 with a gate 195-203 us, 1.2 PFLOP/s, the
+// Measured: 4096 rows 7168 -> 2 x 2048 with a gate 195-205 us, 1.2 PFLOP/s, the
 // matrix unit busy for 0.59 of a CU's busy cycles, no bank conflicts; without the loads
 // into LDS it would take 154, without the reads from LDS 180: what is left is the
 // issue of both beside the products, and the epilogue, during which a CU with one
-// block multiplies nothing (2048 -> 7168 with a residual: 141-147 us for half the
-// products, 0.44).  Both gradients of the first: 207 us each, 1.16 PFLOP/s.
+// block multiplies nothing (2048 -> 7168 with a residual: 136-142 us for half the
+// products, 0.48).  The gradients of the first: 203 and 198 us, 1.2 PFLOP/s, 0.7.
 #include <type_traits>
 
 #include "dense.h"
@@ -687,8 +687,8 @@ hipError_t launch_stream(const Product &p, hipStream_t stream) {
 // its columns over runs of dz_rows rows, for the bias.  A thread takes 8 columns
 // of a row, CG of them (a power of two, 64 at most) a row of up to 512 columns,
 // the block's others further rows, 4 at a time so that their loads are under way
-// together.  4096 rows of 2 x 2048 with silu's gate: 84 MB in 27.6 us, 3.0 TB/s; the
-// vector instructions (some 80 for a pair of results) take two thirds of that.
+// together.  4096 rows of 2 x 2048 with silu's gate: 84 MB in 27.5 us, 3.1 TB/s, of
+// which the vector instructions, 49 for a pair of results, are 11.
 constexpr int kDzThreads = 256;
 // A kernel for each activation: with all of them in one its code alone took a
 // small call 10 us to fetch (100 rows of 512: 18 us).
