@@ -31,7 +31,9 @@ static_assert(sizeof(FewSegment) == 64, "one line");
 
 // The second kernel's blocks have 32 columns of y.  Where those are fewer than
 // the chip's CUs, each has several blocks with a part of the segments, and the
-// last of them adds up the parts.
+// last of them adds up the parts (with parts / without, the layer, us: 64 tokens,
+// 96 experts, 2048 wide, 176 / 260; 4096 wide, 64 experts 233 / 287; 7 tokens, 1000
+// wide, 24 / 32).  Wider layers have blocks enough.
 constexpr int kFewColumns = 32, kFewJoins = 128;
 inline int few_columns(const FewShape &s) { return (s.H + kFewColumns - 1) / kFewColumns; }
 inline int few_parts(const FewShape &s) {

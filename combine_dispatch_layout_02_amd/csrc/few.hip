@@ -596,6 +596,8 @@ struct Work {   // the workspace's parts
 template <bool F8, int RT, int TT>
 hipError_t launch_down(const FewShape &s, const Work &k, const uint8_t *down, const float *downs,
                        const uint16_t *residual, uint16_t *y, hipStream_t stream) {
+    // Half the LDS (two steps ahead, or 4 waves) and twice the blocks: 1 to 9 % faster
+    // for large experts of many tokens, 5 to 11 % slower for few tokens or small ones.
     constexpr int G = kFewColumns / 16, NW = 8, NB = 4;
     const int cols = few_columns(s), parts = few_parts(s);
     hipLaunchKernelGGL((ep_few_down_kernel<F8, RT, TT, G, NW, NB>), dim3((unsigned)(cols * parts)), dim3(64 * NW), 0,
@@ -618,6 +620,10 @@ hipError_t launch(const FewShape &s, const uint16_t *x, const int64_t *idx, cons
                   const float *ups, const uint8_t *down, const float *downs, const uint16_t *residual, uint16_t *y,
                   uint8_t *ws, hipStream_t stream) {
     const Work k(s, ws);
+    // 32 tokens of an expert at a time where they have more than 8 on average, else 16
+    // (the layer, us, 16 / 32 at a time): 64 tokens top-8 of 48 experts 4096 x 1408
+    // 197 / 201, of 32 of 4096 x 2048 237 / 224; 48 tokens top-8 of 16, bf16, 236 / 218;
+    // 64 tokens top-6 of 96 176 / 183.
     const hipError_t e = s.T * s.k > 8 * s.E ? launch_up<F8, 2, 2, 4>(s, k, x, idx, w, up, ups, stream)
                                              : launch_up<F8, 2, 1, 4>(s, k, x, idx, w, up, ups, stream);
     if (e != hipSuccess) return e;
