@@ -321,18 +321,17 @@ __global__ __launch_bounds__(64 * NW) void ep_few_up_kernel(
         const f32x4 v = gates(acc[g][m], acc[GU + g][m]);
         const int r = 16 * m + r16, col = n0 + 16 * g + 4 * quad;
         if (r >= rows || col >= s.I) continue;   // I % 8 == 0: all 4 in or all out
-        // h leaves as two bf16 parts, its upper 16 bits and the rounded rest:
-        // 2^-17 of it is lost, at 4 bytes a value that the caches hold
+        // h leaves as two bf16 parts, rounded to nearest: 2^-17 of it is lost, at 4
+        // bytes a value that the caches hold
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float f = v[q] * rows_w[r];
-            hi[q] = f2u(f) & 0xFFFF0000u;
-            const bool finite = (hi[q] & 0x7F800000u) != 0x7F800000u;
-            lo[q] = finite ? f32_to_bf16(f - u2f(hi[q])) : 0u;
+            float f = v[q] * rows_w[r];
+            hi[q] = take_part(f);
+            lo[q] = f32_to_bf16(f);
         }
         uint16_t *o = h + (size_t)rows_pair[r] * 2 * s.I + col;
-        *reinterpret_cast<uint2 *>(o) = uint2{hi[0] >> 16 | hi[1], hi[2] >> 16 | hi[3]};
+        *reinterpret_cast<uint2 *>(o) = uint2{hi[0] | hi[1] << 16, hi[2] | hi[3] << 16};
         *reinterpret_cast<uint2 *>(o + s.I) = uint2{lo[0] | lo[1] << 16, lo[2] | lo[3] << 16};
     }
 }

@@ -31,6 +31,17 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {
     return o;
 }
 
+// v rounded to bf16, which leaves v with the rest, exactly: the value's next part.
+// Of a value in [1, 2) 2^-8 is left at most after one part, 2^-17 after two, nothing
+// after three.  A finite value's part is finite: cut where it would round up to
+// infinity.
+__device__ __forceinline__ uint32_t take_part(float &v) {
+    uint32_t h = f32_to_bf16(v);
+    if ((h & 0x7FFF) == 0x7F80 && v - v == 0.0f) h = f2u(v) >> 16;
+    v = (h & 0x7F80) == 0x7F80 ? 0.0f : v - u2f(h << 16);
+    return h;
+}
+
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
