@@ -72,8 +72,9 @@ struct LinearShape {
     bool plain() const { return act == kActNone && !gated && !f32; }
 };
 
-// Workspace of the backward pass: dz in bf16 (in three parts for an fp32
-// gradient of the weights) unless it is dy itself, the bias' sums of runs of rows.
+// Workspace of the backward pass: dz in bf16 (in two parts from an fp32 dy, in
+// three for an fp32 gradient of the weights) unless it is dy itself, the bias' sums
+// of runs of rows.
 // Rows of a run, by 512 columns for a block: 64, or fewer (4 at least) where the
 // blocks would not fill the chip (100 rows of 512: 64 rows 15 us, 4 rows 5).
 inline int dz_rows(const LinearShape &s) {
@@ -82,7 +83,7 @@ inline int dz_rows(const LinearShape &s) {
     return r;
 }
 inline size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
-inline int dz_parts(const LinearShape &s) { return s.plain() ? 0 : (s.w32 ? 3 : 1); }
+inline int dz_parts(const LinearShape &s) { return s.plain() ? 0 : (s.w32 ? 3 : (s.f32 ? 2 : 1)); }
 inline size_t linear_sums_offset(const LinearShape &s) {
     return align256((size_t)dz_parts(s) * s.M * s.wide() * 2);
 }

@@ -682,9 +682,13 @@ hipError_t launch_stream(const Product &p, hipStream_t stream) {
 
 // ---------------------------------------------------------------- the gradient over z
 
-// dz from dy and z in bf16 (in one part, or in three: the rounded value, its
+// dz from dy and z in bf16 (in one part, or in two or three: the rounded value, its
 // rounded rest and the rest of that, together the binary32 value) and the sums of
-// its columns over runs of dz_rows rows, for the bias.  A thread takes 8 columns
+// its columns over runs of dz_rows rows, for the bias.  One part where dy is bf16
+// too, as a gradient between two bf16 operators is; two from an fp32 dy, whose
+// precision the caller asks for: they lose 2^-17 of it where one loses 2^-8 (the
+// logits' backward pass, 4096 x 7168 -> 256, takes 95 us with dx in two parts,
+// 84 in one); three where the weights' gradient stays in fp32.  A thread takes 8 columns
 // of a row, CG of them (a power of two, 64 at most) a row of up to 512 columns,
 // the block's others further rows, 4 at a time so that their loads are under way
 // together.  4096 rows of 2 x 2048 with silu's gate: 84 MB in 27.5 us, 3.1 TB/s, of
@@ -722,13 +726,7 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
             for (int i = 0; i < 4; ++i) {
                 uint32_t h[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    float &v = f[2 * i + j];
-                    h[j] = f32_to_bf16(v);
-                    // of several parts the first stays finite where the value is
-                    if (parts > 1 && (h[j] & 0x7FFF) == 0x7F80 && v - v == 0.0f) h[j] = f2u(v) >> 16;
-                    v = (h[j] & 0x7F80) == 0x7F80 ? 0.0f : v - u2f(h[j] << 16);
-                }
+                for (int j = 0; j < 2; ++j) h[j] = take_part(f[2 * i + j]);
                 out[i] = h[0] | h[1] << 16;
             }
             st16(dz + n * plane + at, out);
@@ -879,7 +877,7 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
         return grad_w || grad_bias ? hipGetLastError() : hipSuccess;
     }
     // three parts only for the product that takes them
-    const int parts = s.plain() ? 0 : (s.w32 && grad_w ? 3 : 1);
+    const int two = s.f32 ? 2 : 1, parts = s.plain() ? 0 : (s.w32 && grad_w ? 3 : two);
     uint16_t *dz = reinterpret_cast<uint16_t *>(ws);
     float *sums = reinterpret_cast<float *>(ws + linear_sums_offset(s));
     const int run_rows = dz_rows(s);
@@ -911,7 +909,8 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
     g.x.r = {d, s.M, wide, 0};
     g.x.q = {w, s.K, s.K, 0};
     g.x.k = wide;
-    g.x.parts = 1;
+    g.x.parts = two;
+    g.x.part = s.M * wide;
     g.x.out_ld = s.K;
     g.x.out = grad_x;
     g.w.r = {d, wide, wide, 0};
@@ -927,8 +926,8 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
     // with three of them, 20.5 with one).  Both products' blocks have room on the
     // chip at once (two a CU), and sums below 1024 are those that launch_product does
     // not halve: a gradient that is asked for alone has the same bits.
-    if (grad_x && grad_w && tile_count(g.x, 64, 64) + tile_count(g.w, 64, 64) <= 512 && wide < 1024 &&
-        s.M * g.w.parts < 1024) {
+    if (grad_x && grad_w && tile_count(g.x, 64, 64) + tile_count(g.w, 64, 64) <= 512 &&
+        wide * g.x.parts < 1024 && s.M * g.w.parts < 1024) {
         const auto tiles = [](Product &p) {
             p.rtiles = (int)((p.r.rows + 63) / 64);
             p.ctiles = (int)((p.out_ld + 63) / 64);

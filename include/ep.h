@@ -700,10 +700,13 @@ int ep_linear_backward_workspace_bytes(const ep_linear_shape *shape, size_t *byt
  *     dz = dy * act'(z)     gated: [dy * z[:, N:] * act'(z[:, :N]), dy * act(z[:, :N])]
  *     grad_x = dz w, grad_w = dz^T x, grad_bias = sum over rows of dz
  * (that of the residual is dy itself; relu' is 0 at 0).  dz is computed in fp32.
- * For the two products it is rounded to bf16, half a step of which is what the
- * rounding of their bf16 results is; for an fp32 grad_w it enters as three bf16
- * parts, which lose nothing, unless it is dy itself.  grad_bias is the sum of the
- * fp32 values, in fp32, in a fixed order.  Deterministic for a shape.
+ * For the two products it is rounded to bf16 where dy is bf16, half a step of
+ * which is what the rounding of their bf16 results is; from an fp32 dy it enters
+ * them as two bf16 parts, which lose 2^-17 of it, and for an fp32 grad_w as three,
+ * which lose nothing, unless it is dy itself.  (With several parts, a gradient that
+ * an infinite x or w should make infinite can be NaN, as a part can be 0.)
+ * grad_bias is the sum of the fp32 values, in fp32, in a fixed order.
+ * Deterministic for a shape.
  *   dy [M, N] bf16 or fp32 (y_f32); z [M, N or 2 N] bf16, NULL where there is
  *   neither activation nor gate; x, w as for ep_linear
  *   grad_x [M, K] bf16, grad_w [N or 2 N, K] bf16 or fp32 (grad_w_f32),
