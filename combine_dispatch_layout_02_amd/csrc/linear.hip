@@ -80,6 +80,69 @@ __device__ __forceinline__ void derive(float z, float *f, float *d) {
     }
 }
 
+// The lower tail.  From kTail down e^z, or its like, nears binary32's smallest
+// normal numbers and leaves them, but a factor (a gate's, a gradient) can bring the
+// product back: silu(-96) is 2e-40, of which 3e-4 was lost, and of silu(-103) a
+// quarter, before 1e20 multiplied it.  So there act(z) is f y^2 and act'(z) d y^2, and
+// the factor is multiplied in between the two y, which are normal numbers down to z
+// = -174, -18.6 and -13.0 (below, act(z) u is under 2^-116 for any u).
+template <int ACT>
+constexpr float kTail = ACT == kActSilu ? -80.0f : ACT == kActGelu ? -12.0f : ACT == kActGeluTanh ? -9.7f : 0.0f;
+template <int ACT>
+struct Tail {
+    float y, f, d;
+    __device__ __forceinline__ explicit Tail(float z) {
+        if constexpr (ACT == kActGelu) {
+            // erfc by its asymptotic series (Abramowitz and Stegun 7.1.23): the first
+            // term left out is 945 / z^10, 1.5e-8
+            const float r = __builtin_amdgcn_rcpf(z), w = r * r;
+            const float s = kPdf * (1.0f - w * (1.0f - w * (3.0f - w * (15.0f - w * 105.0f))));
+            y = expf(-0.25f * z * z);
+            f = -s;
+            d = kPdf * z - s * r;
+        } else if constexpr (ACT == kActGeluTanh) {
+            y = expf(0.5f * (kTanhArg * (z + 0.044715f * z * z * z)));
+            f = z;
+            const float near = fmaxf(z, -20.0f);   // y is 0 from there on
+            d = 1.0f + near * (kTanhArg * (1.0f + 3 * 0.044715f * near * near));
+        } else {
+            y = expf(0.5f * z);
+            f = z;
+            d = 1.0f + z;
+        }
+    }
+    __device__ __forceinline__ float value(float u) const { return f * y * u * y; }
+    // dy u act'(z); dy u may leave binary32 above
+    __device__ __forceinline__ float slope(float dy, float u) const {
+        const float s = dy * u;
+        return __builtin_isfinite(s) ? s * y * d * y : dy * y * (u * y) * d;
+    }
+};
+// Whether a lane of the wave has one of its 8 values there: the others' time is one
+// comparison of their least.
+template <int ACT>
+__device__ __forceinline__ bool any_in_tail(const float (&z)[8]) {
+    if constexpr (kTail<ACT> == 0.0f) return false;
+    float least = z[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) least = fminf(least, z[i]);
+    return __ballot(least < kTail<ACT>) != 0;
+}
+// z[i] becomes act(z[i]) u[i].
+template <int ACT>
+__device__ __forceinline__ void activate8(float (&z)[8], const float (&u)[8]) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(z[i]) * u[i];
+    if (any_in_tail<ACT>(z)) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (z[i] < kTail<ACT>) v[i] = Tail<ACT>(z[i]).value(u[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = v[i];
+}
+
 // f(std::integral_constant) for the activation, the same for every lane.
 template <int V>
 struct Const {
@@ -255,13 +318,12 @@ __device__ __forceinline__ void finish(const Product &p, int64_t r, int64_t c, E
             v.store(p.z + (p.gated ? at + r * p.out_ld : at));
             if (p.gated) u.store(p.z + at + (r + 1) * p.out_ld);
         }
-        with_activation(p.act, [&](auto act) {
+        if (p.gated || p.act != kActNone) {
+            if (!p.gated)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v.v[i] = activate<decltype(act)::value>(v.v[i]);
-        });
-        if (p.gated)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v.v[i] *= u.v[i];
+                for (int i = 0; i < 8; ++i) u.v[i] = 1.0f;
+            with_activation(p.act, [&](auto act) { activate8<decltype(act)::value>(v.v, u.v); });
+        }
         if (p.residual) v.add(residual);
     }
     v.store(p.out, p.out_f32, at);
@@ -762,6 +824,15 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
                 derive<ACT>(v[j], &f, &d);
                 a[j] = GATED ? g[j] * u[j] * d : g[j] * d;
                 if (GATED) b[j] = g[j] * f;
+            }
+            if (any_in_tail<ACT>(v)) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (v[j] < kTail<ACT>) {
+                        const Tail<ACT> t(v[j]);
+                        a[j] = t.slope(g[j], GATED ? u[j] : 1.0f);
+                        if (GATED) b[j] = t.value(g[j]);
+                    }
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) sum[0][j] += a[j], sum[1][j] += b[j];
