@@ -822,7 +822,8 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
             for (int j = 0; j < 8; ++j) {
                 float f, d;
                 derive<ACT>(v[j], &f, &d);
-                a[j] = GATED ? g[j] * u[j] * d : g[j] * d;
+                const float gu = GATED ? g[j] * u[j] : g[j];
+                a[j] = ACT == kActRelu ? (v[j] <= 0.0f ? 0.0f : gu) : gu * d;   // gu may be infinite beside a closed gate
                 if (GATED) b[j] = g[j] * f;
             }
             if (any_in_tail<ACT>(v)) {

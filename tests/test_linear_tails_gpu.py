@@ -118,3 +118,17 @@ def test_lowest_values(ep):
                                        bias=True)
         assert torch.isfinite(gb).all() and torch.isfinite(gw).all()
         assert (gb.cpu()[:8][far] == 0).all() and (gb.cpu()[8:][far] == 0).all()
+
+
+def test_closed_relu_gate(ep):
+    """dy u past binary32 behind a closed gate: the gradient is 0, not NaN."""
+    z = torch.tensor([-1.0, 0.0, -0.0, -3e38, 2.0, 1e-30, -1e-30, 1.0])
+    u = torch.tensor([1e30, -1e30, 3e38, 1e30, 1e5, 1e5, 1e30, -2.0])
+    dy = torch.full((1, 8), 1e20, device="cuda")
+    x, w = torch.ones(1, 8, dtype=BF, device="cuda"), torch.ones(16, 8, dtype=BF, device="cuda")
+    zu = torch.cat((z, u)).to(BF)
+    gx, gw, gb = ep.linear_backward(dy, x, w, zu[None].cuda(), "relu", True, bias=True)
+    zd, ud = zu[:8].double(), zu[8:].double()
+    want = torch.cat((torch.where(zd > 0, 1e20 * ud, 0), 1e20 * zd.clamp(min=0)))
+    _close(gb, want, torch.full_like(want, 2 * ref.STEP), ref.F32_HALF)
+    assert torch.isfinite(gx).all() and torch.isfinite(gw).all()
