@@ -900,9 +900,11 @@ __global__ __launch_bounds__(256) void ep_linear_gradients_kernel(Gradients g) {
         add_runs(g.sums, g.runs, g.wide, g.bias, blockIdx.x - g.xblocks - g.wblocks);
 }
 
+// At most kZeroBlocks blocks: a launch has to stay below 2^32 threads, and 16 bytes
+// for each end at 64 GiB.
+constexpr int64_t kZeroBlocks = 1 << 16;
 __global__ __launch_bounds__(256) void ep_linear_zero_kernel(vec16 *out, int64_t n) {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) out[i] = vec16{};
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) out[i] = vec16{};
 }
 
 }  // namespace
@@ -940,8 +942,9 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
     if (s.M == 0) {
         if (grad_w) {
             const int64_t n = (int64_t)wide * s.K * (s.w32 ? 4 : 2) / 16;
-            hipLaunchKernelGGL(ep_linear_zero_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream,
-                               static_cast<vec16 *>(grad_w), n);
+            const int64_t blocks = (n + 255) / 256;
+            hipLaunchKernelGGL(ep_linear_zero_kernel, dim3((unsigned)(blocks < kZeroBlocks ? blocks : kZeroBlocks)),
+                               dim3(256), 0, stream, static_cast<vec16 *>(grad_w), n);
         }
         if (grad_bias)
             hipLaunchKernelGGL(ep_linear_bias_kernel, dim3((unsigned)((wide + 15) / 16)), dim3(256), 0, stream,
