@@ -364,15 +364,15 @@ struct Tile {
     typedef Side<TQ, BC, W, KS> Q;
     static constexpr int RBYTES = P * R::BYTES, BYTES = RBYTES + Q::BYTES;
     static_assert(SK == 1 || (W * NC * NR * 1024 <= SK * BYTES && SK <= NB + 1), "a buffer takes the sums of a part");
-    static __device__ __forceinline__ void run(const Product &p, uint32_t block);
+    static constexpr int BUFFERS = NB, LDS = SK * BYTES;   // of each buffer
+    // The buffers are the kernel's, one array each, so that the compiler can tell them apart.
+    static __device__ __forceinline__ void run(const Product &p, uint32_t block, uint8_t *buf0, uint8_t *buf1,
+                                               uint8_t *buf2, uint8_t *buf3);
 };
 
 template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK, int P>
-__device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK, P>::run(const Product &p, uint32_t block) {
-    __shared__ __attribute__((aligned(16))) uint8_t buf0[SK * BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t buf1[SK * BYTES];
-    __shared__ __attribute__((aligned(16))) uint8_t buf2[NB > 2 ? SK * BYTES : 16];
-    __shared__ __attribute__((aligned(16))) uint8_t buf3[NB > 3 ? SK * BYTES : 16];
+__device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK, P>::run(
+    const Product &p, uint32_t block, uint8_t *buf0, uint8_t *buf1, uint8_t *buf2, uint8_t *buf3) {
     const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int wid = wave % W, sk = wave / W;
     const auto buf = [&](int j) {
@@ -528,7 +528,11 @@ __device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK, 
 
 template <typename T>
 __global__ __launch_bounds__(T::THREADS) void ep_linear_tile_kernel(Product p) {
-    T::run(p, blockIdx.x);
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[T::LDS];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[T::LDS];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[T::BUFFERS > 2 ? T::LDS : 16];
+    __shared__ __attribute__((aligned(16))) uint8_t buf3[T::BUFFERS > 3 ? T::LDS : 16];
+    T::run(p, blockIdx.x, buf0, buf1, buf2, buf3);
 }
 
 template <bool TR, bool TQ, bool GATED, int BR, int BC, int WR, int WC, int KS, int NB, int SK = 1, int P = 1>
@@ -859,8 +863,7 @@ __global__ __launch_bounds__(kDzThreads) void ep_linear_dz_kernel(LinearShape s,
 // The runs' sums: 16 columns a block and 16 threads to a column, each with a 16th
 // of the runs, added in order; with no runs, 0.
 __device__ __forceinline__ void add_runs(const float *__restrict__ sums, int64_t runs, int wide, float *__restrict__ out,
-                                         uint32_t block) {
-    __shared__ float part[16][16];
+                                         uint32_t block, float (*part)[16]) {
     const int lane = threadIdx.x % 16, group = threadIdx.x / 16, c = block * 16 + lane;
     float v = 0.0f;
     if (c < wide)
@@ -875,7 +878,8 @@ __device__ __forceinline__ void add_runs(const float *__restrict__ sums, int64_t
 }
 __global__ __launch_bounds__(256) void ep_linear_bias_kernel(const float *__restrict__ sums, int64_t runs, int wide,
                                                              float *__restrict__ out) {
-    add_runs(sums, runs, wide, out, blockIdx.x);
+    __shared__ float part[16][16];
+    add_runs(sums, runs, wide, out, blockIdx.x, part);
 }
 
 // The three gradients of a small call in one launch: blocks of the one over x,
@@ -892,12 +896,20 @@ typedef Tile<false, true, false, 64, 64, 4, 1, 64, 4, 1, 1> SmallX;
 typedef Tile<true, true, false, 64, 64, 4, 1, 64, 4, 1, 1> SmallW;
 __global__ __launch_bounds__(256) void ep_linear_gradients_kernel(Gradients g) {
     static_assert(SmallX::THREADS == 256 && SmallW::THREADS == 256, "one kind of block");
+    static_assert(SmallX::BUFFERS == 4 && SmallW::BUFFERS == 4, "the same buffers for all");
+    constexpr int LDS = SmallX::LDS > SmallW::LDS ? SmallX::LDS : SmallW::LDS;
+    static_assert(2 * 4 * LDS <= 160 * 1024, "two blocks a CU");
+    __shared__ __attribute__((aligned(16))) uint8_t buf0[LDS];
+    __shared__ __attribute__((aligned(16))) uint8_t buf1[LDS];
+    __shared__ __attribute__((aligned(16))) uint8_t buf2[LDS];
+    __shared__ __attribute__((aligned(16))) uint8_t buf3[LDS];
     if (blockIdx.x < g.xblocks)
-        SmallX::run(g.x, blockIdx.x);
+        SmallX::run(g.x, blockIdx.x, buf0, buf1, buf2, buf3);
     else if (blockIdx.x - g.xblocks < g.wblocks)
-        SmallW::run(g.w, blockIdx.x - g.xblocks);
+        SmallW::run(g.w, blockIdx.x - g.xblocks, buf0, buf1, buf2, buf3);
     else
-        add_runs(g.sums, g.runs, g.wide, g.bias, blockIdx.x - g.xblocks - g.wblocks);
+        add_runs(g.sums, g.runs, g.wide, g.bias, blockIdx.x - g.xblocks - g.wblocks,
+                 reinterpret_cast<float (*)[16]>(buf0));
 }
 
 // At most kZeroBlocks blocks: a launch has to stay below 2^32 threads, and 16 bytes
@@ -997,10 +1009,14 @@ hipError_t launch_linear_backward(const LinearShape &s, const void *dy, const ui
     g.w.out = grad_w;
     g.w.out_f32 = s.w32;
     const unsigned columns = grad_bias ? (unsigned)((wide + 15) / 16) : 0;
-    // Small calls: what counts is the launches (100 rows 512 -> 512: 28.1 us for all
-    // with three of them, 20.5 with one).  Both products' blocks have room on the
-    // chip at once (two a CU), and sums below 1024 are those that launch_product does
-    // not halve: a gradient that is asked for alone has the same bits.
+    // Small calls: what counts is the launches.  One for all three against three of
+    // them, with dz's, us: 100 rows 1000 -> 512 (160 tiles) 10.1 / 15.6, 340 rows 1536
+    // -> 512 (336) 10.6 / 17.4, 1000 rows 1024 -> 960 (496) 18.2 / 25.2, 1000 rows 1000
+    // -> 1000 (512) 23.8 / 29.3.  Up to 512 tiles both products' blocks have room on
+    // the chip at once: two a CU, as all kinds of blocks share one set of buffers, 66
+    // KiB (with a set for each, 132, those cases took 10.2, 13.3, 23.2 and 27.5).  And
+    // sums below 1024 are those that launch_product does not halve: a gradient that
+    // is asked for alone has the same bits.
     if (grad_x && grad_w && tile_count(g.x, 64, 64) + tile_count(g.w, 64, 64) <= 512 &&
         wide * g.x.parts < 1024 && s.M * g.w.parts < 1024) {
         const auto tiles = [](Product &p) {
