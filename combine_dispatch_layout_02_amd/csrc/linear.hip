@@ -128,16 +128,16 @@ __device__ __forceinline__ bool any_in_tail(const float (&z)[8]) {
     for (int i = 1; i < 8; ++i) least = fminf(least, z[i]);
     return __ballot(least < kTail<ACT>) != 0;
 }
-// z[i] becomes act(z[i]) u[i].
-template <int ACT>
+// z[i] becomes act(z[i]) u[i], or act(z[i]).
+template <int ACT, bool GATED>
 __device__ __forceinline__ void activate8(float (&z)[8], const float (&u)[8]) {
     float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = activate<ACT>(z[i]) * u[i];
+    for (int i = 0; i < 8; ++i) v[i] = GATED ? activate<ACT>(z[i]) * u[i] : activate<ACT>(z[i]);
     if (any_in_tail<ACT>(z)) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (z[i] < kTail<ACT>) v[i] = Tail<ACT>(z[i]).value(u[i]);
+            if (z[i] < kTail<ACT>) v[i] = Tail<ACT>(z[i]).value(GATED ? u[i] : 1.0f);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = v[i];
@@ -307,23 +307,19 @@ struct Eight {
 };
 
 // The last steps of 8 results at row r, columns c .. c + 7 (gated: their factors in u).
+template <bool GATED>
 __device__ __forceinline__ void finish(const Product &p, int64_t r, int64_t c, Eight v, Eight u, vec16 residual) {
     const int64_t at = r * p.out_ld + c;
     if (p.linear) {
         if (p.bias) {
             v.add(p.bias + c);
-            if (p.gated) u.add(p.bias + p.out_ld + c);
+            if (GATED) u.add(p.bias + p.out_ld + c);
         }
         if (p.z) {
-            v.store(p.z + (p.gated ? at + r * p.out_ld : at));
-            if (p.gated) u.store(p.z + at + (r + 1) * p.out_ld);
+            v.store(p.z + (GATED ? at + r * p.out_ld : at));
+            if (GATED) u.store(p.z + at + (r + 1) * p.out_ld);
         }
-        if (p.gated || p.act != kActNone) {
-            if (!p.gated)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) u.v[i] = 1.0f;
-            with_activation(p.act, [&](auto act) { activate8<decltype(act)::value>(v.v, u.v); });
-        }
+        with_activation(p.act, [&](auto act) { activate8<decltype(act)::value, GATED>(v.v, u.v); });
         if (p.residual) v.add(residual);
     }
     v.store(p.out, p.out_f32, at);
@@ -521,7 +517,7 @@ __device__ __forceinline__ void Tile<TR, TQ, GATED, BR, BC, WR, WC, KS, NB, SK, 
 #pragma unroll
         for (int m = 0; m < ROWS; ++m) {
             const Eight v(acc[2 * f][m], acc[2 * f + 1][m]), u(acc[2 * f + HALF][m], acc[2 * f + 1 + HALF][m]);
-            if (inside(f, m)) finish(p, row(m), column(f), v, u, residual[f][m]);
+            if (inside(f, m)) finish<GATED>(p, row(m), column(f), v, u, residual[f][m]);
         }
     }
 }
@@ -711,14 +707,14 @@ __global__ __launch_bounds__(64 * NW) void ep_linear_stream_kernel(Product p, in
             const int c = c0 + 8 * (quad >> 1);
             if (r < rows && quad % 2 == 0 && (!GATED || G > 1 || quad == 0) && c < p.out_ld) {
                 if (p.residual) residual = ld16(p.residual + (r0 + r) * p.out_ld + c);
-                finish(p, r0 + r, c, v, w, residual);
+                finish<GATED>(p, r0 + r, c, v, w, residual);
             }
         } else {
             const int c = c0 + Eight::column(quad);
             const Eight v(sum[0], sum[G - 1]);
             if (r < rows && c < p.out_ld) {
                 if (p.residual) residual = ld16(p.residual + (r0 + r) * p.out_ld + c);
-                finish(p, r0 + r, c, v, v, residual);
+                finish<GATED>(p, r0 + r, c, v, v, residual);
             }
         }
     }

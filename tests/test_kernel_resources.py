@@ -1,6 +1,6 @@
 """What the compiler took for the kernels, from the metadata in the built
 library (no GPU): blocks that launch rules count two to a CU fit twice into its
-160 KiB of LDS."""
+160 KiB of LDS, and the products' kernels spill nothing to memory."""
 import struct
 
 import pytest
@@ -67,3 +67,10 @@ def test_two_blocks_a_cu(kernels):
     for part in ("ep_linear_gradients_kernel", "ep_few_up_kernel"):
         for k in _named(kernels, part):
             assert 2 * k[".group_segment_fixed_size"] <= LDS, k[".name"]
+
+
+@pytest.mark.parametrize("part", ["ep_linear_", "ep_few_"])
+def test_no_scratch(kernels, part):
+    for k in _named(kernels, part):
+        assert k[".group_segment_fixed_size"] <= LDS
+        assert k[".private_segment_fixed_size"] == 0, k[".name"]
