@@ -29,11 +29,14 @@ struct FewSegment {
 };
 static_assert(sizeof(FewSegment) == 64, "one line");
 
-// The second kernel's blocks have 32 columns of y.  Where those are fewer than
-// the chip's CUs, each has several blocks with a part of the segments, and the
-// last of them adds up the parts (with parts / without, the layer, us: 64 tokens,
-// 96 experts, 2048 wide, 176 / 260; 4096 wide, 64 experts 233 / 287; 7 tokens, 1000
-// wide, 24 / 32).  Wider layers have blocks enough.
+// The second kernel's blocks have 32 columns of y.  Up to 128 of them, where at
+// least two for each fit the 256 CUs, each has several blocks with a part of the
+// segments, and the last of them adds up the parts (with parts / without, the layer,
+// us: 64 tokens, 96 experts, 2048 wide, 176 / 260; 4096 wide, 64 experts 233 / 287; 7
+// tokens, 1000 wide, 24 / 32).  From 129 on, two for each come in a second round and
+// cost more than the CUs that one leaves idle: 4224 wide, 64 tokens, top-8 of 32
+// experts 317 / 304, 5120 wide 350 / 346, 7168 wide 384 / 373; one token 50 / 43, 55 /
+// 51, 76 / 71.
 constexpr int kFewColumns = 32, kFewJoins = 128;
 inline int few_columns(const FewShape &s) { return (s.H + kFewColumns - 1) / kFewColumns; }
 inline int few_parts(const FewShape &s) {

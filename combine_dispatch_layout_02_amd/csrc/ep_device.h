@@ -3,7 +3,8 @@
 // Number formats (bit-exact definitions, written for the hardware's integer
 // and IEEE float units; no fast-math, no flush-to-zero):
 //   bf16   : top 16 bits of a binary32; narrowing rounds to nearest even,
-//            NaN becomes 0x7FC0.
+//            NaN becomes 0x7FC0 (in the results of the few tokens' layer and
+//            the dense products: any quiet NaN).
 //   e4m3   : OCP 8-bit float "E4M3" (fn variant): bias 7, 3 mantissa bits,
 //            S.1111.111 = NaN, no infinities, largest finite 448.  Encoding
 //            rounds to nearest even and saturates finite overflow and
@@ -45,8 +46,9 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 // The same two narrowings by gfx950's v_cvt_pk_bf16_f32 (one instruction):
 // round to nearest even, bit for bit f32_to_bf16 on every non-NaN binary32
 // (checked over all 2^32 patterns on MI355X); a NaN keeps its payload
-// (quieted) instead of becoming 0x7FC0, so it is used only where no input is
-// NaN (pack_bf16).
+// (quieted) instead of becoming 0x7FC0, so it is used where no input is NaN
+// (pack_bf16), and for results in which one NaN is as good as another (the few
+// tokens' layer, the dense products and their gradients).
 __device__ __forceinline__ uint32_t pack_bf16x2_cvt(float lo, float hi) {
     const f32x2_t v = {lo, hi};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));

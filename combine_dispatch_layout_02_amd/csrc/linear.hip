@@ -16,7 +16,7 @@
 // matrix unit busy for 0.59 of a CU's busy cycles, no bank conflicts; without the loads
 // into LDS it would take 154, without the reads from LDS 180: what is left is the
 // issue of both beside the products, and the epilogue, during which a CU with one
-// block multiplies nothing (2048 -> 7168 with a residual: 136-142 us for half the
+// block multiplies nothing (2048 -> 7168 with a residual: 124-142 us for half the
 // products, 0.48).  The gradients of the first: 203 and 198 us, 1.2 PFLOP/s, 0.7.
 #include <type_traits>
 
@@ -555,6 +555,11 @@ int64_t tile_count(const Product &p, int BR, int BC) {
 //   2048 rows 2048 -> 7168       256 x 256 tiles 73, 128 x 128 80
 //   1024 rows 7168 -> 2048       64 x 128 (256 tiles) 37.5, 128 x 128 (128) 62, 64 x 64 (512) 46
 //   512 rows 4096 -> 4096        64 x 128 (256) 24.0, 128 x 128 (128) 37.6, 64 x 64 (512) 27.5
+// The rule leaves the sums' length out; of 4096 rows by 7168 and by 4096 columns (448
+// and 256 of the largest tiles), 256 x 256 / 128 x 128: K = 64 31.4 / 37.6 and 20.2 /
+// 23.8, 256 38.0 / 36.9 and 23.4 / 22.2, 512 49.3 / 47.5 and 28.8 / 28.5, 1024 70.6 / 75.0
+// and 40.2 / 43.9; dx of 4096 x 7168 from K = 128 22.5 / 35.7, 256 28.0 / 35.9, 512 38.6 /
+// 46.7.
 // The weights' gradient, whose operands both come by lines of k, gains by 256 x 128
 // in between (4096 x 2048 from 4096 rows 62, 128 x 128 72; 2560 x 2048 from 16384
 // rows 171 / 221), the other products lose (2048 rows 4096 -> 4096 77 / 73).
@@ -566,6 +571,10 @@ int64_t tile_count(const Product &p, int BR, int BC) {
 // steps each, if those are 16 or more:
 //   64 rows 7168 -> 2048 x 2 27.9, halved 24.3;  100 rows 4096 -> 4096 18.1, 16.1
 //   300 rows 4096 -> 1024    17.8, halved 15.5;  512 rows 7168 -> 256  28.6, 24.9
+// Shorter sums lose by it (512 rows by 1024: K = 256 4.7, halved 5.7, 512 5.5 / 5.8, 1024
+// 7.3 / 7.1).  Past 128 tiles, with a CU's LDS full of one block, it would still gain where
+// sums are long: 768 rows by 1024 (192 tiles) K = 1024 7.4, halved 7.3, 2048 11.1 / 10.0,
+// 7168 28.3 / 24.5; 256 tiles 7168 29.0 / 26.5.
 template <bool TR, bool TQ, bool GATED>
 hipError_t launch_product(const Product &p, hipStream_t stream) {
     const auto tiles = [&](int BR, int BC) { return tile_count(p, BR, BC); };
